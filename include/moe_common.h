@@ -1,6 +1,6 @@
 /*
- * moe_common.h -- types shared by the four MoE block libraries
- * (moe_router, moe_dispatch, moe_experts, moe_combine).
+ * moe_common.h -- types shared by the MoE block libraries (moe_router,
+ * moe_dispatch, moe_experts, moe_combine; moe_train for training).
  *
  * The block is the forward pass of one DeepSeek-V3/R1 Mixture-of-Experts FFN
  * layer as the pages "DeepSeek-V3.2-Exp · Router" and "DeepSeek-V3.2-Exp ·

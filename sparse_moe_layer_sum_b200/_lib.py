@@ -1,5 +1,5 @@
-"""ctypes loader for the four C-ABI libraries (moe_router, moe_dispatch,
-moe_experts, moe_combine).  Loading fails loudly: there is no fallback."""
+"""ctypes loader for the five C-ABI libraries (moe_router, moe_dispatch,
+moe_experts, moe_combine, moe_train).  Loading fails loudly: there is no fallback."""
 from __future__ import annotations
 
 import ctypes
@@ -44,8 +44,16 @@ class MoEEpShard(ctypes.Structure):
     _fields_ = [("rank", ctypes.c_int32), ("world", ctypes.c_int32)]
 
 
+class MoEGroupedShape(ctypes.Structure):
+    """Mirror of moe_grouped_shape in include/moe_train.h."""
+
+    _fields_ = [("groups", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("rows", ctypes.c_int64)]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _cfgp = ctypes.POINTER(MoECfg)
+_gsp = ctypes.POINTER(MoEGroupedShape)
 
 # (library, symbol) -> (restype, argtypes); this is the full exported C-ABI
 SIGNATURES = {
@@ -87,9 +95,25 @@ SIGNATURES = {
     ("moe_experts", "moe_experts_set_profile_events"): (_i32, [ctypes.POINTER(_vp), _i32]),
     ("moe_experts", "moe_experts_selftest_wait"): (_i32, [_i64, _vp, _vp]),
     ("moe_combine", "moe_combine"): (_i32, [_cfgp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("moe_train", "moe_grouped_linear"): (
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    ("moe_train", "moe_grouped_linear_dx"): (
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
+    ("moe_train", "moe_grouped_linear_dw"): (
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp]),
+    ("moe_train", "moe_checkpoint_rows"): (_i32, [_vp, _i32, _i64, _i32, _vp, _vp, _vp]),
+    ("moe_train", "moe_restore_rows"): (
+        _i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _vp, _vp]),
+    ("moe_train", "moe_swiglu_checkpoint_workspace_size"): (_sz, [_gsp, _i32]),
+    ("moe_train", "moe_swiglu_checkpoint"): (
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    ("moe_train", "moe_swiglu_backward_workspace_size"): (_sz, [_gsp, _i32]),
+    ("moe_train", "moe_swiglu_backward"): (
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+               _vp, _vp]),
 }
 
-LIBRARIES = ("moe_router", "moe_dispatch", "moe_experts", "moe_combine")
+LIBRARIES = ("moe_router", "moe_dispatch", "moe_experts", "moe_combine", "moe_train")
 
 _libs: dict[str, ctypes.CDLL] = {}
 

@@ -1,4 +1,4 @@
-"""Builds the four C-ABI libraries in-tree for sm_100a with nvcc.
+"""Builds the five C-ABI libraries in-tree for sm_100a with nvcc.
 
     python -m sparse_moe_layer_sum_b200.build [--verbose]
 
@@ -24,6 +24,7 @@ LIBRARIES = {
     "moe_dispatch": "dispatch.cu",
     "moe_experts": "experts.cu",
     "moe_combine": "combine.cu",
+    "moe_train": "train.cu",
 }
 
 NVCC_FLAGS = [
@@ -64,7 +65,7 @@ def build_one(name: str, src: str, verbose: bool = False, force: bool = False) -
 
 def build_all(verbose: bool = False, force: bool = False) -> list[str]:
     os.makedirs(LIBDIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=4) as ex:
+    with ThreadPoolExecutor(max_workers=5) as ex:
         futs = [ex.submit(build_one, n, s, verbose, force) for n, s in LIBRARIES.items()]
         return [f.result() for f in futs]
 

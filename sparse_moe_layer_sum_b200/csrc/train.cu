@@ -1,0 +1,296 @@
+// moe_train: training operators of the experts (moe_train.h) -- host checks,
+// the choice of kernel and the launches.
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include "ckpt.cuh"
+#include "common.cuh"
+#include "grouped.cuh"
+#include "grouped_simt.cuh"
+#include "moe_train.h"
+
+namespace moe {
+namespace {
+
+using grouped::bf16;
+using grouped::Table;
+
+bool act_type(moe_dtype dt) { return dt == MOE_BF16 || dt == MOE_F32; }
+size_t elem(moe_dtype dt) { return dt == MOE_F32 ? 4 : 2; }
+
+moe_status check_shape(const moe_grouped_shape *s) {
+  if (!s) return MOE_ERR_INVALID;
+  if (s->groups < 1 || s->n < 1 || s->k < 1 || s->rows < 0) return MOE_ERR_INVALID;
+  if (s->groups > grouped::MAX_GROUPS || s->n > (1 << 20) || s->k > (1 << 20) ||
+      s->rows >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
+  // tile numbers are 32-bit: 64-row tiles of 64 columns at the finest
+  const int64_t cols = s->n > s->k ? s->n : s->k;
+  if ((s->rows / 16 + s->groups) * ((cols + 63) / 64) >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
+
+// ------------------------------------------------------------ CUDA-core path
+
+template <typename TI, typename TO, int DIR, int B>
+moe_status launch_simt(const simt::Args &a, int64_t tiles, int nsm, cudaStream_t s) {
+  const size_t smem = simt::smem_bytes<B>(a.G);
+  const int64_t grid = tiles < (int64_t)nsm * 4 ? tiles : (int64_t)nsm * 4;
+  simt::product<TI, TO, DIR, B><<<(unsigned)grid, simt::THREADS, smem, s>>>(a);
+  return launch_status();
+}
+
+template <typename TI, typename TO, int DIR>
+moe_status simt_tiles(const simt::Args &a, cudaStream_t s) {
+  const int nsm = sm_count();
+  if (nsm < 1) return MOE_ERR_CUDA;
+  const int cols = DIR == simt::LIN ? a.n : a.k;
+  auto tiles = [&](int b) {
+    const int64_t ct = (cols + b - 1) / b;
+    return DIR == simt::DW ? (int64_t)a.G * ((a.n + b - 1) / b) * ct : (a.rows / b + a.G) * ct;
+  };
+  // 128 x 128 tiles reuse each operand value twice as often as 64 x 64 ones;
+  // the smaller tiles where the larger would leave SMs without work
+  if (tiles(128) >= 2 * nsm) return launch_simt<TI, TO, DIR, 128>(a, tiles(128), nsm, s);
+  return launch_simt<TI, TO, DIR, 64>(a, tiles(64), nsm, s);
+}
+
+template <int DIR>
+moe_status simt_product(const simt::Args &a, moe_dtype in, moe_dtype out, cudaStream_t s) {
+  if (in == MOE_F32)
+    return out == MOE_F32 ? simt_tiles<float, float, DIR>(a, s) : simt_tiles<float, bf16, DIR>(a, s);
+  return out == MOE_F32 ? simt_tiles<bf16, float, DIR>(a, s) : simt_tiles<bf16, bf16, DIR>(a, s);
+}
+
+// ------------------------------------------------------------------ products
+
+struct Product {
+  const moe_grouped_shape *s;
+  moe_dtype dt, out_dt;
+  const void *a0, *b0, *a1, *b1;  // rows and weights (dw: dy and x)
+  const int32_t *offsets;
+  void *out;
+  int accumulate;
+  int32_t *status;
+  cudaStream_t stream;
+};
+
+simt::Args simt_args(const Product &p) {
+  simt::Args a;
+  a.a0 = p.a0;
+  a.b0 = p.b0;
+  a.a1 = p.a1;
+  a.b1 = p.b1;
+  a.c = p.out;
+  a.offsets = p.offsets;
+  a.G = p.s->groups;
+  a.n = p.s->n;
+  a.k = p.s->k;
+  a.rows = p.s->rows;
+  a.accumulate = p.accumulate;
+  a.status = p.status;
+  return a;
+}
+
+moe_status run_linear(const Product &p) {
+  return simt_product<simt::LIN>(simt_args(p), p.dt, p.out_dt, p.stream);
+}
+
+moe_status run_dx(const Product &p) {
+  return simt_product<simt::DX>(simt_args(p), p.dt, p.out_dt, p.stream);
+}
+
+moe_status run_dw(const Product &p) {
+  return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
+}
+
+unsigned row_grid(int64_t warps) {
+  const int64_t blocks = (warps + ckpt::ROW_THREADS / 32 - 1) / (ckpt::ROW_THREADS / 32);
+  const int64_t most = 148 * 8;
+  return (unsigned)(blocks < most ? blocks : most);
+}
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_EXPORT moe_status moe_grouped_linear(const moe_grouped_shape *s, const void *x, moe_dtype dt,
+                                         const void *w, const int32_t *offsets, void *y,
+                                         moe_dtype y_dt, int32_t *dev_status,
+                                         moe_stream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (!act_type(dt) || !act_type(y_dt)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0) return MOE_OK;
+  if (!x || !w || !offsets || !y) return MOE_ERR_INVALID;
+  return run_linear({s, dt, y_dt, x, w, nullptr, nullptr, offsets, y, 0, dev_status,
+                     as_stream(stream)});
+}
+
+MOE_EXPORT moe_status moe_grouped_linear_dx(const moe_grouped_shape *s, const void *dy,
+                                            moe_dtype dt, const void *w, const void *dy2,
+                                            const void *w2, const int32_t *offsets, void *dx,
+                                            moe_dtype dx_dt, int32_t *dev_status,
+                                            moe_stream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (!act_type(dt) || !act_type(dx_dt)) return MOE_ERR_UNSUPPORTED;
+  if ((dy2 == nullptr) != (w2 == nullptr)) return MOE_ERR_INVALID;
+  if (s->rows == 0) return MOE_OK;
+  if (!dy || !w || !offsets || !dx) return MOE_ERR_INVALID;
+  return run_dx({s, dt, dx_dt, dy, w, dy2, w2, offsets, dx, 0, dev_status, as_stream(stream)});
+}
+
+MOE_EXPORT moe_status moe_grouped_linear_dw(const moe_grouped_shape *s, const void *dy,
+                                            moe_dtype dt, const void *x, const int32_t *offsets,
+                                            void *dw, moe_dtype dw_dt, int32_t accumulate,
+                                            int32_t *dev_status, moe_stream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (!act_type(dt) || !act_type(dw_dt)) return MOE_ERR_UNSUPPORTED;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID;
+  // without rows the row buffers may be empty (NULL), but dw is still written
+  if (!offsets || !dw || (s->rows > 0 && (!dy || !x))) return MOE_ERR_INVALID;
+  return run_dw({s, dt, dw_dt, dy, x, nullptr, nullptr, offsets, dw, accumulate, dev_status,
+                 as_stream(stream)});
+}
+
+MOE_EXPORT moe_status moe_checkpoint_rows(const void *src, moe_dtype dt, int64_t rows, int32_t k,
+                                          uint8_t *codes, uint8_t *exps, moe_stream_t stream) {
+  if (rows < 0 || k < 1) return MOE_ERR_INVALID;
+  if (rows >= ((int64_t)1 << 31) || k > (1 << 20) || !act_type(dt)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!src || !codes || !exps) return MOE_ERR_INVALID;
+  cudaStream_t cs = as_stream(stream);
+  const int nb = (k + ckpt::BLOCK - 1) / ckpt::BLOCK;
+  if (k % 8 == 0 && aligned(src, 16) && aligned(codes, 8)) {
+    const int per = 32 * ckpt::UNROLL;
+    const unsigned grid = row_grid(rows * ((nb * 4 + per - 1) / per));
+    if (dt == MOE_F32)
+      ckpt::save_rows_v8<<<grid, ckpt::ROW_THREADS, 0, cs>>>(static_cast<const float *>(src), rows, k, codes, exps);
+    else
+      ckpt::save_rows_v8<<<grid, ckpt::ROW_THREADS, 0, cs>>>(static_cast<const bf16 *>(src), rows, k, codes, exps);
+    return launch_status();
+  }
+  const unsigned grid = row_grid(rows * nb);
+  if (dt == MOE_F32)
+    ckpt::save_rows<<<grid, ckpt::ROW_THREADS, 0, cs>>>(static_cast<const float *>(src), rows, k, codes, exps);
+  else
+    ckpt::save_rows<<<grid, ckpt::ROW_THREADS, 0, cs>>>(static_cast<const bf16 *>(src), rows, k, codes, exps);
+  return launch_status();
+}
+
+MOE_EXPORT moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps, int64_t rows,
+                                       int32_t k, const int32_t *index, int64_t n, void *out,
+                                       moe_dtype out_dt, int32_t *dev_status,
+                                       moe_stream_t stream) {
+  if (rows < 0 || n < 0 || k < 1) return MOE_ERR_INVALID;
+  if (rows >= ((int64_t)1 << 31) || n >= ((int64_t)1 << 31) || k > (1 << 20) || !act_type(out_dt))
+    return MOE_ERR_UNSUPPORTED;
+  if (!index && n > rows) return MOE_ERR_INVALID;
+  if (n == 0) return MOE_OK;
+  if (!out || (rows > 0 && (!codes || !exps))) return MOE_ERR_INVALID;
+  cudaStream_t cs = as_stream(stream);
+  const int nb = (k + ckpt::BLOCK - 1) / ckpt::BLOCK;
+  if (k % 8 == 0 && aligned(out, 16) && aligned(codes, 8)) {
+    const int per = 32 * ckpt::UNROLL;
+    const unsigned grid = row_grid(n * ((nb * 4 + per - 1) / per));
+    if (out_dt == MOE_F32)
+      ckpt::load_rows_v8<<<grid, ckpt::ROW_THREADS, 0, cs>>>(codes, exps, rows, k, index, n, static_cast<float *>(out), dev_status);
+    else
+      ckpt::load_rows_v8<<<grid, ckpt::ROW_THREADS, 0, cs>>>(codes, exps, rows, k, index, n, static_cast<bf16 *>(out), dev_status);
+    return launch_status();
+  }
+  const unsigned grid = row_grid(n * nb);
+  if (out_dt == MOE_F32)
+    ckpt::load_rows<<<grid, ckpt::ROW_THREADS, 0, cs>>>(codes, exps, rows, k, index, n, static_cast<float *>(out), dev_status);
+  else
+    ckpt::load_rows<<<grid, ckpt::ROW_THREADS, 0, cs>>>(codes, exps, rows, k, index, n, static_cast<bf16 *>(out), dev_status);
+  return launch_status();
+}
+
+MOE_EXPORT size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt) {
+  if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
+  // the two projections in fp32
+  return 2 * align_up((size_t)s->rows * s->n * 4, 256);
+}
+
+MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const void *x,
+                                            moe_dtype dt, const void *w1, const void *w3,
+                                            const int32_t *offsets, void *h, uint8_t *codes_a,
+                                            uint8_t *exps_a, uint8_t *codes_u, uint8_t *exps_u,
+                                            void *ws, size_t ws_bytes, int32_t *dev_status,
+                                            moe_stream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (!act_type(dt)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0) return MOE_OK;
+  if (!x || !w1 || !w3 || !offsets || !h || !codes_a || !exps_a || !codes_u || !exps_u)
+    return MOE_ERR_INVALID;
+  if (!ws || ws_bytes < moe_swiglu_checkpoint_workspace_size(s, dt)) return MOE_ERR_WORKSPACE;
+  cudaStream_t cs = as_stream(stream);
+  float *a = static_cast<float *>(ws);
+  float *u = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + align_up((size_t)s->rows * s->n * 4, 256));
+  if ((st = run_linear({s, dt, MOE_F32, x, w1, nullptr, nullptr, offsets, a, 0, dev_status, cs})) != MOE_OK)
+    return st;
+  if ((st = run_linear({s, dt, MOE_F32, x, w3, nullptr, nullptr, offsets, u, 0, dev_status, cs})) != MOE_OK)
+    return st;
+  const ckpt::Saved sv{codes_a, exps_a, codes_u, exps_u};
+  const unsigned grid = row_grid(s->rows * ((s->n + ckpt::BLOCK - 1) / ckpt::BLOCK));
+  if (dt == MOE_F32)
+    ckpt::swiglu_save<<<grid, ckpt::ROW_THREADS, 0, cs>>>(a, u, offsets, s->groups, s->rows, s->n, static_cast<float *>(h), sv);
+  else
+    ckpt::swiglu_save<<<grid, ckpt::ROW_THREADS, 0, cs>>>(a, u, offsets, s->groups, s->rows, s->n, static_cast<bf16 *>(h), sv);
+  return launch_status();
+}
+
+MOE_EXPORT size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt) {
+  if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
+  return align_up((size_t)s->rows * s->n * 4, 256);  // dh in fp32
+}
+
+MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
+                                          const void *w2, const uint8_t *codes_a,
+                                          const uint8_t *exps_a, const uint8_t *codes_u,
+                                          const uint8_t *exps_u, const float *gate,
+                                          const int32_t *offsets, void *da, void *du, void *hg,
+                                          float *dgate, void *ws, size_t ws_bytes,
+                                          int32_t *dev_status, moe_stream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (!act_type(dt)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0) return MOE_OK;
+  if (!dy || !w2 || !codes_a || !exps_a || !codes_u || !exps_u || !offsets || !da || !du || !hg ||
+      !dgate)
+    return MOE_ERR_INVALID;
+  if (!ws || ws_bytes < moe_swiglu_backward_workspace_size(s, dt)) return MOE_ERR_WORKSPACE;
+  cudaStream_t cs = as_stream(stream);
+  float *dh = static_cast<float *>(ws);
+  // dh = dy w2: the input gradient of a linear layer from n features to k
+  const moe_grouped_shape lin{s->groups, s->k, s->n, s->rows};
+  if ((st = run_dx({&lin, dt, MOE_F32, dy, w2, nullptr, nullptr, offsets, dh, 0, dev_status, cs})) != MOE_OK)
+    return st;
+  const ckpt::Saved sv{const_cast<uint8_t *>(codes_a), const_cast<uint8_t *>(exps_a),
+                       const_cast<uint8_t *>(codes_u), const_cast<uint8_t *>(exps_u)};
+  const unsigned grid = row_grid(s->rows * (ckpt::ROW_THREADS / 32));
+  if (dt == MOE_F32)
+    ckpt::swiglu_grads<<<grid, ckpt::ROW_THREADS, 0, cs>>>(
+        dh, sv, gate, offsets, s->groups, s->rows, s->n, static_cast<float *>(da),
+        static_cast<float *>(du), static_cast<float *>(hg), dgate);
+  else
+    ckpt::swiglu_grads<<<grid, ckpt::ROW_THREADS, 0, cs>>>(
+        dh, sv, gate, offsets, s->groups, s->rows, s->n, static_cast<bf16 *>(da),
+        static_cast<bf16 *>(du), static_cast<bf16 *>(hg), dgate);
+  return launch_status();
+}

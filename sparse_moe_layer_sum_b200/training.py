@@ -1,0 +1,255 @@
+"""Python binding of the experts' training operators (moe_train).
+
+Argument marshalling only, as in moe.py.  Row buffers are expert-contiguous:
+group g owns rows offsets[g] .. offsets[g + 1] - 1, the order dispatch_build
+produces.  Every function allocates its outputs (or takes them as `out`),
+enqueues on the current stream of the operands' device and does not
+synchronise; rows outside the groups are left as they were.
+
+    y  = grouped_linear(x, w, offsets)                    # y = x w^T, by group
+    dx = grouped_linear_dx(dy, w, offsets)                # dx = dy w
+    dw = grouped_linear_dw(dy, x, offsets)                # dw = dy^T x
+    h, a, u = swiglu_checkpoint(x, w1, w3, offsets)       # a, u kept in 8 bits
+    da, du, hg, dgate = swiglu_backward(dy, w2, a, u, offsets, gate=gate)
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _lib
+from ._lib import MoEGroupedShape, check, fn
+from .moe import _ptr
+
+_DT = {torch.float32: _lib.DTYPES["f32"], torch.bfloat16: _lib.DTYPES["bf16"]}
+SCALE_BLOCK = 32  # values of a row that share a scale
+
+
+@dataclass
+class Checkpoint:
+    """Rows kept in 8 bits: e4m3 codes [rows, k] (uint8) and one biased
+    power-of-two exponent for 32 values, exps [rows, ceil(k / 32)] (uint8);
+    value = e4m3(code) * 2^(exp - 127)."""
+
+    codes: torch.Tensor
+    exps: torch.Tensor
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.exps.numel()
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _check(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
+    dev = first.device
+    for t in (first, *others):
+        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors")
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _call(dev: torch.device, sym: str, *args) -> None:
+    """Call `sym` of moe_train with `dev` current, on its current stream."""
+    f = fn("moe_train", sym)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream().cuda_stream)
+    check(st, sym)
+
+
+def _groups(offsets: torch.Tensor) -> int:
+    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2,
+          "offsets must be int32 [groups + 1]")
+    return offsets.numel() - 1
+
+
+def _dtype(t: torch.Tensor, *others: torch.Tensor) -> int:
+    _need(t.dtype in _DT, "operands must be bf16 or fp32")
+    _need(all(o.dtype == t.dtype for o in others), "operands must have one dtype")
+    return _DT[t.dtype]
+
+
+def _out(out, shape, dtype, dev) -> torch.Tensor:
+    _need(dtype in _DT, "outputs must be bf16 or fp32")
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(tuple(out.shape) == tuple(shape) and out.dtype == dtype, "out has another shape or dtype")
+    return out
+
+
+def _status(status: Optional[torch.Tensor]) -> Optional[int]:
+    if status is not None:
+        _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32")
+    return _ptr(status)
+
+
+def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
+                   out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                   status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_grouped_linear: y[p] = x[p] w[g]^T for the rows p of each group g.
+    x [rows, k], w [groups, n, k] -> y [rows, n] (x's dtype unless out_dtype)."""
+    dev = _check(x, w, offsets, out, status)
+    G = _groups(offsets)
+    _need(x.dim() == 2 and w.dim() == 3 and w.shape[0] == G and w.shape[2] == x.shape[1],
+          "x must be [rows, k] and w [groups, n, k]")
+    dt = _dtype(x, w)
+    rows, n = x.shape[0], w.shape[1]
+    out = _out(out, (rows, n), out_dtype or (x.dtype if out is None else out.dtype), dev)
+    _call(dev, "moe_grouped_linear", ctypes.byref(MoEGroupedShape(G, n, x.shape[1], rows)),
+          x.data_ptr(), dt, w.data_ptr(), offsets.data_ptr(), out.data_ptr(), _DT[out.dtype],
+          _status(status))
+    return out
+
+
+def grouped_linear_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
+                      dy2: Optional[torch.Tensor] = None, w2: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                      status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_grouped_linear_dx: dx[p] = dy[p] w[g] (+ dy2[p] w2[g], in one sum).
+    dy [rows, n], w [groups, n, k] -> dx [rows, k] (dy's dtype unless out_dtype)."""
+    dev = _check(dy, w, dy2, w2, offsets, out, status)
+    G = _groups(offsets)
+    _need(dy.dim() == 2 and w.dim() == 3 and w.shape[0] == G and w.shape[1] == dy.shape[1],
+          "dy must be [rows, n] and w [groups, n, k]")
+    _need((dy2 is None) == (w2 is None), "dy2 and w2 come together")
+    dt = _dtype(dy, w)
+    if dy2 is not None:
+        _need(dy2.shape == dy.shape and w2.shape == w.shape, "dy2 and w2 must match dy and w")
+        _dtype(dy, dy2, w2)
+    rows, k = dy.shape[0], w.shape[2]
+    out = _out(out, (rows, k), out_dtype or (dy.dtype if out is None else out.dtype), dev)
+    _call(dev, "moe_grouped_linear_dx", ctypes.byref(MoEGroupedShape(G, w.shape[1], k, rows)),
+          dy.data_ptr(), dt, w.data_ptr(), _ptr(dy2), _ptr(w2), offsets.data_ptr(),
+          out.data_ptr(), _DT[out.dtype], _status(status))
+    return out
+
+
+def grouped_linear_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, *,
+                      out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                      accumulate: bool = False,
+                      status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_grouped_linear_dw: dw[g] = sum over the group's rows of dy^T x, added
+    to `out` with accumulate.  dy [rows, n], x [rows, k] -> dw [groups, n, k]
+    (dy's dtype unless out_dtype); zero for a group without rows."""
+    dev = _check(dy, x, offsets, out, status)
+    G = _groups(offsets)
+    _need(dy.dim() == 2 and x.dim() == 2 and x.shape[0] == dy.shape[0],
+          "dy must be [rows, n] and x [rows, k]")
+    _need(out is not None or not accumulate, "accumulate needs out")
+    dt = _dtype(dy, x)
+    (rows, n), k = dy.shape, x.shape[1]
+    out = _out(out, (G, n, k), out_dtype or (dy.dtype if out is None else out.dtype), dev)
+    _call(dev, "moe_grouped_linear_dw", ctypes.byref(MoEGroupedShape(G, n, k, rows)),
+          dy.data_ptr(), dt, x.data_ptr(), offsets.data_ptr(), out.data_ptr(), _DT[out.dtype],
+          int(accumulate), _status(status))
+    return out
+
+
+def _blocks(k: int) -> int:
+    return -(-k // SCALE_BLOCK)
+
+
+def _empty_ckpt(rows: int, k: int, dev) -> Checkpoint:
+    return Checkpoint(torch.empty(rows, k, dtype=torch.uint8, device=dev),
+                      torch.empty(rows, _blocks(k), dtype=torch.uint8, device=dev))
+
+
+def _check_ckpt(c: Checkpoint, rows: int, k: int) -> None:
+    _need(c.codes.dtype == torch.uint8 and c.exps.dtype == torch.uint8
+          and tuple(c.codes.shape) == (rows, k) and tuple(c.exps.shape) == (rows, _blocks(k)),
+          "a checkpoint holds uint8 codes [rows, k] and exps [rows, ceil(k / 32)]")
+
+
+def checkpoint_rows(src: torch.Tensor) -> Checkpoint:
+    """moe_checkpoint_rows: src [rows, k] (bf16 or fp32) kept in 8 bits."""
+    dev = _check(src)
+    _need(src.dim() == 2, "src must be [rows, k]")
+    dt = _dtype(src)
+    rows, k = src.shape
+    c = _empty_ckpt(rows, k, dev)
+    _call(dev, "moe_checkpoint_rows", src.data_ptr(), dt, rows, k, c.codes.data_ptr(),
+          c.exps.data_ptr())
+    return c
+
+
+def restore_rows(ckpt: Checkpoint, index: Optional[torch.Tensor] = None, *,
+                 dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_restore_rows: the stored rows [n, k], row index[i] at place i (int32;
+    every row in order without index)."""
+    dev = _check(ckpt.codes, ckpt.exps, index, out, status)
+    _need(ckpt.codes.dim() == 2, "codes must be [rows, k]")
+    rows, k = ckpt.codes.shape
+    _check_ckpt(ckpt, rows, k)
+    if index is not None:
+        _need(index.dtype == torch.int32 and index.dim() == 1, "index must be int32 [n]")
+    n = rows if index is None else index.numel()
+    out = _out(out, (n, k), dtype if out is None else out.dtype, dev)
+    _call(dev, "moe_restore_rows", ckpt.codes.data_ptr(), ckpt.exps.data_ptr(), rows, k,
+          _ptr(index), n, out.data_ptr(), _DT[out.dtype], _status(status))
+    return out
+
+
+def _workspace(sym: str, shape: MoEGroupedShape, dt: int, dev):
+    need = fn("moe_train", sym)(ctypes.byref(shape), dt)
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+def swiglu_checkpoint(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, offsets: torch.Tensor, *,
+                      status: Optional[torch.Tensor] = None):
+    """moe_swiglu_checkpoint: (h, a, u) with h = silu(x w1^T) * (x w3^T) by group
+    [rows, n] and the two projections as Checkpoints.  x [rows, k],
+    w1, w3 [groups, n, k]."""
+    dev = _check(x, w1, w3, offsets, status)
+    G = _groups(offsets)
+    _need(x.dim() == 2 and w1.dim() == 3 and w1.shape[0] == G and w1.shape[2] == x.shape[1]
+          and w3.shape == w1.shape, "x must be [rows, k], w1 and w3 [groups, n, k]")
+    dt = _dtype(x, w1, w3)
+    rows, n = x.shape[0], w1.shape[1]
+    h = torch.empty(rows, n, dtype=x.dtype, device=dev)
+    a, u = _empty_ckpt(rows, n, dev), _empty_ckpt(rows, n, dev)
+    shape = MoEGroupedShape(G, n, x.shape[1], rows)
+    ws = _workspace("moe_swiglu_checkpoint_workspace_size", shape, dt, dev)
+    _call(dev, "moe_swiglu_checkpoint", ctypes.byref(shape), x.data_ptr(), dt, w1.data_ptr(),
+          w3.data_ptr(), offsets.data_ptr(), h.data_ptr(), a.codes.data_ptr(), a.exps.data_ptr(),
+          u.codes.data_ptr(), u.exps.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+          _status(status))
+    return h, a, u
+
+
+def swiglu_backward(dy: torch.Tensor, w2: torch.Tensor, a: Checkpoint, u: Checkpoint,
+                    offsets: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None):
+    """moe_swiglu_backward: (da, du, hg, dgate) of gate * (h w2^T) for the h of a
+    checkpoint.  dy [rows, k], w2 [groups, k, n], gate [rows] fp32 (1 without)
+    -> da, du, hg [rows, n] in dy's dtype, dgate [rows] fp32."""
+    dev = _check(dy, w2, a.codes, a.exps, u.codes, u.exps, gate, offsets, status)
+    G = _groups(offsets)
+    _need(dy.dim() == 2 and w2.dim() == 3 and w2.shape[0] == G and w2.shape[1] == dy.shape[1],
+          "dy must be [rows, k] and w2 [groups, k, n]")
+    dt = _dtype(dy, w2)
+    (rows, k), n = dy.shape, w2.shape[2]
+    _check_ckpt(a, rows, n)
+    _check_ckpt(u, rows, n)
+    if gate is not None:
+        _need(gate.dtype == torch.float32 and tuple(gate.shape) == (rows,), "gate must be fp32 [rows]")
+    da, du, hg = (torch.empty(rows, n, dtype=dy.dtype, device=dev) for _ in range(3))
+    dgate = torch.empty(rows, dtype=torch.float32, device=dev)
+    shape = MoEGroupedShape(G, n, k, rows)
+    ws = _workspace("moe_swiglu_backward_workspace_size", shape, dt, dev)
+    _call(dev, "moe_swiglu_backward", ctypes.byref(shape), dy.data_ptr(), dt, w2.data_ptr(),
+          a.codes.data_ptr(), a.exps.data_ptr(), u.codes.data_ptr(), u.exps.data_ptr(), _ptr(gate),
+          offsets.data_ptr(), da.data_ptr(), du.data_ptr(), hg.data_ptr(), dgate.data_ptr(),
+          _ptr(ws), 0 if ws is None else ws.numel(), _status(status))
+    return da, du, hg, dgate
