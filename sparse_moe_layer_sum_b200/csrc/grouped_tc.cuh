@@ -1,0 +1,851 @@
+// Grouped products on the tcgen05 tensor cores (bf16 operands, fp32 sums).
+//
+// Two persistent, warp-specialised kernels fed by TMA.  Warp 0 streams
+// operand tiles into a ring of shared-memory stages, one thread of warp 1
+// issues the MMAs into tensor memory, and the other warps finish the tiles.
+//
+// rows_gemm -- results with one row per input row (LIN, DX, UP, BWD).  The
+//   weights are the MMA's A operand (128 features per SM and MMA) and the
+//   group's rows its B operand, because N is a run-time field of the
+//   instruction: a tile spends tensor work only on the rows its group has,
+//   rounded up to 16.  LIN and UP contract over the weights' contiguous
+//   index (K-major tiles); DX and BWD over the other one, which the MMA
+//   reads from MN-major tiles, so no transposed copy of a weight exists.
+// dw_gemm -- weight gradients.  The contraction runs over the group's rows,
+//   so both operands are MN-major.  A group ends anywhere inside a tile: the
+//   rows behind it are zeroed in shared memory up to the next multiple of 16
+//   (both operands: the next group may hold infinities), and the MMAs beyond
+//   are not issued.
+#pragma once
+
+#include <cuda.h>
+
+#include "ckpt.cuh"
+#include "grouped.cuh"
+#include "sm100.cuh"
+
+namespace moe {
+namespace tcg {
+
+using namespace grouped;
+using namespace sm100;
+
+constexpr int BK = 64;               // contraction depth of a stage
+constexpr int BM = 128;              // features of one MMA tile and SM
+constexpr int BOX = 64 * BK * 2;     // a 64 x 64 box: 8 KB
+constexpr int TILE = BM * BK * 2;    // an A tile: 16 KB
+constexpr int64_t WAIT_NS = 1000000000LL;
+
+// ------------------------------------------------------------- PTX wrappers
+
+// 3-D tiled load; completion is counted on an mbarrier given by its
+// shared::cluster address (CG 2: of either CTA of the pair).
+template <int CG>
+__device__ __forceinline__ void load_3d(const CUtensorMap *m, void *dst, uint32_t bar, int x, int y,
+                                        int z, uint64_t pol) {
+  if (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void load_2d(const CUtensorMap *m, void *dst, uint32_t bar, int x, int y,
+                                        uint64_t pol) {
+  if (CG == 2)
+    tma_load_2d_pair(m, dst, bar, x, y, pol);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "l"(pol)
+        : "memory");
+}
+
+__device__ __forceinline__ void store_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Arrive with cluster-scope release on a barrier of either CTA of the pair.
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// MN-major operand tile as TMA SWIZZLE_128B boxes of 64 (contiguous) x BK
+// write it: 8-row groups of the contraction index 1024 bytes apart (stride
+// offset), the next 64 contiguous values one box further (leading offset).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((uint32_t)BOX >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;  // instruction descriptor: MN-major operands
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (CG == 2)
+    mma_bf16_pair(d, a, b, idesc, acc);
+  else
+    mma_bf16(d, a, b, idesc, acc);
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar) {  // CG 2: on both CTAs' barriers
+  if (CG == 2)
+    mma_commit_pair_mc(bar, 0x3);
+  else
+    mma_commit(bar);
+}
+
+// Waits for copies or MMAs in flight before the block leaves, with a limit
+// but regardless of the abort flag.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if ((int64_t)(globaltimer_ns() - t0) > WAIT_NS) break;
+}
+__device__ __forceinline__ void pause_ns(int64_t ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while ((int64_t)(globaltimer_ns() - t0) < ns) {
+  }
+}
+
+// A whole warp waits: lane 0 polls and tells the others, so that the lanes
+// cannot disagree about a wait that runs out.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                          int32_t *status) {
+  int ok = 1;
+  if (threadIdx.x % 32 == 0) ok = wait_bounded(bar, parity, abort, WAIT_NS, status);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+struct Ring {  // position in a ring of stages
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ uint8_t *align_smem(uint8_t *raw) {
+  return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                     ~static_cast<uintptr_t>(1023));
+}
+
+// ----------------------------------------------------------------- rows_gemm
+
+enum Op { LIN, DX, UP, BWD };
+
+struct RowParams {
+  const int32_t *offsets;
+  int G, F;          // F: features (columns of the result)
+  int kb0, kb;       // k-blocks of the first source, of all sources
+  int64_t rows;
+  void *out;         // LIN, DX: [rows, F]; UP: h
+  int32_t *status;
+  ckpt::Saved saved;  // UP: written; BWD: read
+  const float *gate;  // BWD, may be NULL
+  bf16 *da, *du, *hg;
+  float *part;        // BWD: [ceil(F / 32), rows] terms of dgate
+};
+
+// CG: SMs per tile.  AT: A tiles per SM (UP: one of w1 and the same rows of
+// w3; LIN, DX: two blocks of features, which halves the row bytes each weight
+// byte is paired with).  BN: rows of a tile.
+template <int OP, int CG, int AT, int BN, int STAGES>
+struct RowCfg {
+  static constexpr bool KMAJOR = OP == LIN || OP == UP;
+  static constexpr int EPI = BN >= 128 ? 8 : 4;  // epilogue warps
+  static constexpr int NT = 32 * (2 + EPI);
+  static constexpr int BROWS = BN / CG;  // rows of the B tile in one SM
+  static constexpr int BOXN = BROWS < 32 ? BROWS : 32;
+  static constexpr int A_ALL = AT * TILE;
+  static constexpr int STAGE = A_ALL + BROWS * BK * 2;
+  static constexpr int FEAT = (OP == UP ? BM : AT * BM) * CG;
+  static constexpr int ACC = AT * BN;
+  static constexpr int NBUF = 2 * ACC <= 512 ? 2 : 1;
+  static constexpr int COLS = NBUF * ACC;
+  static constexpr uint32_t TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int BAR = STAGES * STAGE;
+  static constexpr int NBARS = 2 * STAGES + 5;
+  static constexpr int MISC = BAR + NBARS * 8;
+  static constexpr int TAB = (MISC + 16 + 4 * STAGES + 15) / 16 * 16;
+  static size_t smem(int G) { return 1024 + TAB + Table::bytes(G); }
+  static_assert(BROWS % BOXN == 0 && BOXN % 8 == 0, "row boxes");
+  static_assert(NBUF * ACC <= 512, "tensor memory columns");
+  static_assert(OP != UP || AT == 2, "UP pairs w1 and w3");
+};
+
+// The sum over the 32 lanes of each of 32 values; lane j returns value j's.
+__device__ __forceinline__ float lane_sums(float (&v)[32]) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? v[i] : v[i + w];
+      const float keep = up ? v[i + w] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+    }
+  }
+  return v[0];
+}
+
+template <int OP, int CG, int AT, int BN, int STAGES, typename TO>
+__global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES>::NT, 1)
+    rows_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+              const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+              const RowParams p) {
+  using C = RowCfg<OP, CG, AT, BN, STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = align_smem(smem_raw);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::BAR), *empty = full + STAGES;
+  uint64_t *accf = empty + STAGES, *acce = accf + 2, *drained = acce + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 4);
+  volatile int *pending = reinterpret_cast<volatile int *>(sm + C::MISC + 16);
+  const Table tab(sm + C::TAB, p.G);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const bool leader = rank == 0;
+  const int unit = CG == 2 ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int nunits = CG == 2 ? (int)cluster_count_x() : (int)gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+      pending[s] = -1;
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf + b, 1);
+      mbar_init(acce + b, C::EPI * CG);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA0);
+    tma_prefetch_desc(&tmB0);
+  }
+  if (warp == 1) {
+    if (CG == 2) {
+      tmem_alloc_pair(tmem_slot, C::TMEM);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM);
+      tmem_relinquish();
+    }
+  }
+  build_table(tab, p.offsets, p.G, p.rows, BN, (p.F + C::FEAT - 1) / C::FEAT, p.status);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();  // the pair's barriers exist before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int total = tab.start[p.G];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer
+      // a weight tile that several row tiles of its group read is kept in L2,
+      // one that is read once leaves first; the rows are read by every
+      // feature tile
+      const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
+      const uint64_t pol_b = policy_evict_last();
+      Ring r;
+      bool ok = true;
+      for (int tile = unit; ok && tile < total; tile += nunits) {
+        const Tile t = find_tile(tab, tile, p.G);
+        const uint64_t pol_a = t.ntt > 1 ? keep : once;
+        const int brows = ((t.nvalid + 15) & ~15) / CG;  // this SM's share
+        const int b0 = t.row0 + (int)rank * brows;
+        const int f0 = t.ft * C::FEAT + (int)rank * BM;
+        const int nbox = (brows + C::BOXN - 1) / C::BOXN;
+        const uint32_t bytes = (uint32_t)(C::A_ALL + nbox * C::BOXN * BK * 2);
+        // tiles that run together start at different k-blocks, which spreads
+        // their reads of shared operands over L2
+        const int k0 = (t.ft * 7 + t.tt * 5) % p.kb;
+        for (int i = 0; i < p.kb; ++i) {
+          const int kb = k0 + i < p.kb ? k0 + i : k0 + i - p.kb;
+          if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
+            ok = false;
+            break;
+          }
+          // the leader's barrier counts the bytes of both SMs
+          if (leader) mbar_arrive_expect_tx(full + r.stage, bytes * CG);
+          pending[r.stage] = (int)r.phase;
+          uint8_t *a = sm + r.stage * C::STAGE, *b = a + C::A_ALL;
+          const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(full + r.stage), 0) : smem_u32(full + r.stage);
+          const bool second = kb >= p.kb0;
+          const int kk = (second ? kb - p.kb0 : kb) * BK;
+          const CUtensorMap *ma = second ? &tmA1 : &tmA0, *mb = second ? &tmB1 : &tmB0;
+#pragma unroll
+          for (int i2 = 0; i2 < AT; ++i2) {
+            const int f = f0 + (OP == UP ? 0 : i2 * BM * CG);
+            if (C::KMAJOR) {
+              load_3d<CG>(OP == UP && i2 == 1 ? &tmA1 : ma, a + i2 * TILE, bar, kk, f, t.g, pol_a);
+            } else {
+              load_3d<CG>(ma, a + i2 * TILE, bar, f, kk, t.g, pol_a);
+              load_3d<CG>(ma, a + i2 * TILE + BOX, bar, f + 64, kk, t.g, pol_a);
+            }
+          }
+          for (int j = 0; j < nbox; ++j)
+            load_2d<CG>(mb, b + j * C::BOXN * BK * 2, bar, kk, b0 + j * C::BOXN, pol_b);
+          r.next(STAGES);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // -------------------------------------------------------- MMA issuer
+      Ring r, acc;
+      bool ok = true;
+      for (int tile = unit; ok && tile < total; tile += nunits) {
+        const Tile t = find_tile(tab, tile, p.G);
+        if (!wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc.stage * C::ACC);
+        const uint32_t idesc =
+            idesc_bf16_f32(BM * CG, (t.nvalid + 15) & ~15) | (C::KMAJOR ? 0u : A_MN);
+        for (int kb = 0; kb < p.kb; ++kb) {
+          if (!wait_bounded(full + r.stage, r.phase, abort_flag, WAIT_NS, p.status)) {
+            ok = false;
+            break;
+          }
+          pending[r.stage] = -1;
+          tc_fence_after();
+          const uint32_t a = smem_u32(sm + r.stage * C::STAGE), b = a + C::A_ALL;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t bd = sdesc_sw128(b + kk * 32);
+#pragma unroll
+            for (int i = 0; i < AT; ++i) {
+              const uint64_t ad = C::KMAJOR ? sdesc_sw128(a + i * TILE + kk * 32)
+                                            : desc_mn(a + i * TILE + kk * 2048);
+              mma<CG>(d + i * BN, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+            }
+          }
+          commit<CG>(empty + r.stage);
+          r.next(STAGES);
+        }
+        if (!ok) break;
+        commit<CG>(accf + acc.stage);
+        acc.next(C::NBUF);
+      }
+      if (!ok) {  // no MMA may still write tensor memory when it is freed
+        if (CG == 2)
+          mma_commit_pair(drained);
+        else
+          mma_commit(drained);
+        drain(drained, 0);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;               // TMEM lane quarter of this warp
+    const int half = (warp - 2) >> 2;     // alternate 32-row chunks with 8 warps
+    constexpr int STEP = 32 * (C::EPI / 4);
+    const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
+    Ring acc;
+    for (int tile = unit; tile < total; tile += nunits) {
+      const Tile t = find_tile(tab, tile, p.G);
+      if (!wait_warp(accf + acc.stage, acc.phase, abort_flag, p.status)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.stage * C::ACC);
+      auto release = [&]() {  // hands the accumulator back to the MMA
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            mbar_arrive_cluster(mapa_shared(smem_u32(acce + acc.stage), 0));
+          else
+            mbar_arrive(acce + acc.stage);
+        }
+      };
+      // 32-row chunks of this warp
+      const int nch = t.nvalid > half * 32 ? (t.nvalid - half * 32 + STEP - 1) / STEP : 0;
+      const int fw = t.ft * C::FEAT + (int)rank * BM + q * 32;  // the warp's first feature
+      if (OP == LIN || OP == DX) {
+        // chunks are read in batches; the accumulator goes back right after
+        // the last batch's reads, so its stores overlap the next tile's MMAs
+        constexpr int NB = C::EPI == 8 ? 4 : 2;
+        const int nall = AT * nch;
+        if (nall == 0) release();
+        for (int i0 = 0; i0 < nall; i0 += NB) {
+          uint32_t v[NB][32];
+#pragma unroll
+          for (int u = 0; u < NB; ++u)
+            if (i0 + u < nall)
+              tmem_ld_32x32b_x32(tb + (uint32_t)((i0 + u) / nch * BN + half * 32 + (i0 + u) % nch * STEP), v[u]);
+          tmem_wait_ld();
+          if (i0 + NB >= nall) release();
+#pragma unroll
+          for (int u = 0; u < NB; ++u)
+            if (i0 + u < nall) {
+              const int f = fw + (i0 + u) / nch * BM * CG + lane;
+              const int c0 = half * 32 + (i0 + u) % nch * STEP;
+              TO *o = static_cast<TO *>(p.out) + (size_t)(t.row0 + c0) * p.F + f;
+              if (f < p.F) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (c0 + j < t.nvalid) o[(size_t)j * p.F] = from_f<TO>(__uint_as_float(v[u][j]));
+              }
+            }
+        }
+      } else if (OP == UP) {
+        // a lane holds one hidden feature for 32 rows, the warp the 32
+        // features of one scale block: the block's largest magnitude is one
+        // warp reduction per row
+        const int f = fw + lane;
+        for (int ch = 0; ch < nch; ++ch) {
+          const int c0 = half * 32 + ch * STEP;
+          uint32_t va[32], vu[32];
+          tmem_ld_32x32b_x32(tb + (uint32_t)c0, va);
+          tmem_ld_32x32b_x32(tb + (uint32_t)(BN + c0), vu);
+          tmem_wait_ld();
+          if (ch + 1 == nch) release();
+          const size_t at0 = (size_t)(t.row0 + c0) * p.F + f;
+          int ea = 0, eu = 0;  // lane j keeps row j's scales
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float a = __uint_as_float(va[j]), u = __uint_as_float(vu[j]);
+            const int ja = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(a)));
+            const int ju = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(u)));
+            if (lane == j) {
+              ea = ja;
+              eu = ju;
+            }
+            if (c0 + j < t.nvalid && f < p.F) {
+              const size_t at = at0 + (size_t)j * p.F;
+              static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(a * ckpt::sigmoid<bf16>(a) * u);
+              const uint16_t c = f32x2_to_e4m3x2(ckpt::scaled(a, ckpt::inv_scale_of(ja)),
+                                                 ckpt::scaled(u, ckpt::inv_scale_of(ju)));
+              p.saved.ca[at] = (uint8_t)(c & 0xffu);
+              p.saved.cu[at] = (uint8_t)(c >> 8);
+            }
+          }
+          if (c0 + lane < t.nvalid && fw < p.F) {
+            const size_t at = (size_t)(t.row0 + c0 + lane) * nb + fw / ckpt::BLOCK;
+            p.saved.ea[at] = (uint8_t)ea;
+            p.saved.eu[at] = (uint8_t)eu;
+          }
+        }
+        if (nch == 0) release();
+      } else {  // BWD
+        for (int a = 0; a < AT; ++a) {
+          const int fa = fw + a * BM * CG, f = fa + lane;
+          for (int ch = 0; ch < nch; ++ch) {
+            const int c0 = half * 32 + ch * STEP;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tb + (uint32_t)(a * BN + c0), v);
+            // lane j: the scales and the gate of row j
+            const bool mine = c0 + lane < t.nvalid && fa < p.F;
+            const size_t sat = (size_t)(t.row0 + c0 + lane) * nb + fa / ckpt::BLOCK;
+            const int ea = mine ? p.saved.ea[sat] : 0, eu = mine ? p.saved.eu[sat] : 0;
+            const float gt = mine && p.gate ? p.gate[t.row0 + c0 + lane] : 1.0f;
+            const size_t at0 = (size_t)(t.row0 + c0) * p.F + f;
+            tmem_wait_ld();
+            if (a + 1 == AT && ch + 1 == nch) release();
+            float term[32];
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 16) {
+              uint8_t qa[16], qu[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const bool on = c0 + j0 + j < t.nvalid && f < p.F;
+                const size_t at = at0 + (size_t)(j0 + j) * p.F;
+                qa[j] = on ? p.saved.ca[at] : 0;
+                qu[j] = on ? p.saved.cu[at] : 0;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int r = j0 + j;
+                const float2 d = ckpt::decode2((uint16_t)(qa[j] | qu[j] << 8));
+                const float av = d.x * ckpt::scale_of(__shfl_sync(0xffffffffu, ea, r));
+                const float uv = d.y * ckpt::scale_of(__shfl_sync(0xffffffffu, eu, r));
+                const float g = __shfl_sync(0xffffffffu, gt, r);
+                float xa, xu, xh;
+                const float s = ckpt::swiglu_grad<bf16>(av, uv, __uint_as_float(v[r]), g, xa, xu, xh);
+                term[r] = f < p.F ? s : 0.0f;
+                if (c0 + r < t.nvalid && f < p.F) {
+                  const size_t at = at0 + (size_t)r * p.F;
+                  p.da[at] = __float2bfloat16_rn(xa);
+                  p.du[at] = __float2bfloat16_rn(xu);
+                  p.hg[at] = __float2bfloat16_rn(xh);
+                }
+              }
+            }
+            const float sum = lane_sums(term);
+            if (mine) p.part[(size_t)(fa / ckpt::BLOCK) * p.rows + t.row0 + c0 + lane] = sum;
+          }
+        }
+        if (nch == 0) release();
+      }
+      acc.next(C::NBUF);
+    }
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    // a stalled pipeline stopped early: let copies already issued land (the
+    // leader's barriers count both SMs' copies; the other SM allows its own
+    // some time)
+    if (leader) {
+      for (int s = 0; s < STAGES; ++s)
+        if (pending[s] >= 0) drain(full + s, (uint32_t)pending[s]);
+    } else {
+      pause_ns(200000);
+    }
+  }
+  __syncthreads();
+  if (CG == 2) cluster_sync();  // neither SM leaves while the other may touch its memory
+  if (warp == 1) {
+    tc_fence_after();
+    if (CG == 2)
+      tmem_dealloc_pair(tmem, C::TMEM);
+    else
+      tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+// dgate[row] = the sum of its terms over the feature blocks, in order.
+__global__ void __launch_bounds__(256) sum_parts(const float *__restrict__ part,
+                                                 const int32_t *offsets, int G, int64_t rows,
+                                                 int nb, float *__restrict__ dgate) {
+  int64_t lo, hi;
+  ckpt::live_rows(offsets, G, rows, lo, hi);
+  const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (row < lo || row >= hi) return;
+  float s = 0.0f;
+  for (int b = 0; b < nb; ++b) s += part[(size_t)b * rows + row];
+  dgate[row] = s;
+}
+
+// ------------------------------------------------------------------- dw_gemm
+
+struct DwParams {
+  const int32_t *offsets;
+  int G, n, k;
+  int64_t rows;
+  void *dw;
+  int accumulate;
+  int32_t *status;
+};
+
+// A tile of 256 features of dy (128 per SM of the pair) by 256 columns of x.
+template <typename TO>
+struct DwCfg {
+  static constexpr int BN = 256, STAGES = 4, EPI = 8, NT = 32 * (2 + EPI);
+  static constexpr int STAGE = TILE + BN / 2 * BK * 2;  // per SM: 128 + 128 columns
+  static constexpr int CHUNK = 128 / (int)sizeof(TO);   // columns of a 128-byte staging row
+  static constexpr int STG = STAGES * STAGE;            // two 32 x 128-byte buffers per warp
+  static constexpr int BAR = STG + EPI * 2 * 4096;
+  static constexpr int NBARS = 3 * STAGES + 5;
+  static constexpr int MISC = BAR + NBARS * 8;
+  static constexpr int TAB = (MISC + 16 + 4 * STAGES + 15) / 16 * 16;
+  static size_t smem(int G) { return 1024 + TAB + Table::bytes(G); }
+};
+
+template <typename TO>
+__global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
+    dw_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ CUtensorMap tmC, const DwParams p) {
+  using C = DwCfg<TO>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = align_smem(smem_raw);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::BAR), *empty = full + STAGES;
+  uint64_t *tail = empty + STAGES, *accf = tail + STAGES, *acce = accf + 2, *drained = acce + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 4);
+  // per stage: -1, or the phase its copies complete, + 2 when they count on `tail`
+  volatile int *pending = reinterpret_cast<volatile int *>(sm + C::MISC + 16);
+  const Table tab(sm + C::TAB, p.G);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int unit = (int)cluster_id_x(), nunits = (int)cluster_count_x();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 2);
+      mbar_init(empty + s, 1);
+      mbar_init(tail + s, 1);
+      pending[s] = -1;
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf + b, 1);
+      mbar_init(acce + b, C::EPI * 2);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  build_table(tab, p.offsets, p.G, p.rows, 256, 1, p.status);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int ntiles = (p.n + 255) / 256, ktiles = (p.k + 255) / 256;
+  const int64_t total = (int64_t)p.G * ntiles * ktiles;
+
+  struct Job {
+    int g, n0, k0, lo, kc, kb, tail;  // kb: k-blocks; tail: rows of the last one
+    int nmma;                         // columns of the MMA
+  };
+  auto job = [&](int64_t tile) {
+    Job j;
+    j.g = (int)(tile / (ntiles * ktiles));
+    const int local = (int)(tile - (int64_t)j.g * ntiles * ktiles);
+    j.n0 = local / ktiles * 256;
+    j.k0 = local % ktiles * 256;
+    j.lo = tab.lo[j.g];
+    j.kc = tab.n[j.g];
+    j.kb = (j.kc + BK - 1) / BK;
+    j.tail = j.kc - (j.kb - 1) * BK;
+    j.nmma = min(256, (p.k - j.k0 + 31) / 32 * 32);
+    return j;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer
+      const uint64_t pol = policy_evict_last();  // rows are read by every tile of their group
+      Ring r;
+      bool ok = true;
+      for (int64_t tile = unit; ok && tile < total; tile += nunits) {
+        const Job j = job(tile);
+        const int hb = j.nmma / 2, nbox = (hb + 63) / 64;
+        const int n0 = j.n0 + (int)rank * BM, k0 = j.k0 + (int)rank * hb;
+        const uint32_t bytes = (uint32_t)(TILE + nbox * BOX);
+        for (int i = 0; i < j.kb; ++i) {
+          if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
+            ok = false;
+            break;
+          }
+          // a last block that ends inside a 16-row step is completed on each
+          // SM's own `tail` barrier and handed on when its rows are zeroed
+          const bool fix = i == j.kb - 1 && j.tail % 16 != 0;
+          uint32_t bar;
+          if (fix) {
+            mbar_arrive_expect_tx(tail + r.stage, bytes);
+            bar = mapa_shared(smem_u32(tail + r.stage), rank);
+          } else {
+            mbar_arrive(tail + r.stage);
+            if (leader) {
+              mbar_arrive_expect_tx(full + r.stage, bytes * 2);
+              mbar_arrive(full + r.stage);
+            }
+            bar = mapa_shared(smem_u32(full + r.stage), 0);
+          }
+          pending[r.stage] = (int)r.phase + (fix ? 2 : 0);
+          uint8_t *a = sm + r.stage * C::STAGE, *b = a + TILE;
+          const int row = j.lo + i * BK;
+          load_2d<2>(&tmA, a, bar, n0, row, pol);
+          load_2d<2>(&tmA, a + BOX, bar, n0 + 64, row, pol);
+          for (int c = 0; c < nbox; ++c) load_2d<2>(&tmB, b + c * BOX, bar, k0 + c * 64, row, pol);
+          r.next(STAGES);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer (leader), tail rows (both SMs)
+    Ring r, acc;
+    bool ok = true;
+    for (int64_t tile = unit; ok && tile < total; tile += nunits) {
+      const Job j = job(tile);
+      if (j.kb == 0) continue;
+      if (leader) {
+        if (!wait_warp(acce + acc.stage, acc.phase ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const uint32_t d = tmem + (uint32_t)(acc.stage * 256);
+      const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
+      for (int i = 0; i < j.kb; ++i) {
+        uint8_t *st = sm + r.stage * C::STAGE;
+        const bool fix = i == j.kb - 1 && j.tail % 16 != 0;
+        // the SM that issues no MMAs follows the ring on its `tail` barriers
+        if ((fix || !leader) && !wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        if (fix) {
+          // rows tail .. next multiple of 16 of every 64-column box: 128
+          // bytes each, whole rows, so the swizzle does not matter
+          const int nz = 16 - j.tail % 16, nbox = 2 + (j.nmma / 2 + 63) / 64;
+          for (int z = lane; z < nbox * nz * 8; z += 32) {
+            const int bx = z / (nz * 8), w = z % (nz * 8);
+            *reinterpret_cast<uint4 *>(st + bx * BOX + (j.tail + w / 8) * 128 + w % 8 * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            pending[r.stage] = -1;
+            arrive_cluster(mapa_shared(smem_u32(full + r.stage), 0));
+          }
+        }
+        if (leader) {
+          if (!wait_warp(full + r.stage, r.phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            pending[r.stage] = -1;
+            const uint32_t a = smem_u32(st), b = a + TILE;
+            const int steps = i == j.kb - 1 ? (j.tail + 15) / 16 : BK / 16;
+            for (int s = 0; s < steps; ++s)
+              mma<2>(d, desc_mn(a + s * 2048), desc_mn(b + s * 2048), idesc, (i | s) != 0 ? 1u : 0u);
+            commit<2>(empty + r.stage);
+          }
+          __syncwarp();
+        }
+        r.next(STAGES);
+      }
+      if (!ok) break;
+      if (leader && lane == 0) commit<2>(accf + acc.stage);
+      __syncwarp();
+      acc.next(2);
+    }
+    if (!ok && leader && lane == 0) {
+      mma_commit_pair(drained);
+      drain(drained, 0);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t *stg = sm + C::STG + (warp - 2) * 2 * 4096;
+    int buf = 0;
+    Ring acc;
+    for (int64_t tile = unit; tile < total; tile += nunits) {
+      const Job j = job(tile);
+      if (j.kb == 0 && p.accumulate) continue;
+      const int n0 = j.n0 + (int)rank * BM + q * 32;
+      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.stage * 256 + half * 128);
+      if (j.kb > 0) {
+        if (!wait_warp(accf + acc.stage, acc.phase, abort_flag, p.status)) break;
+        tc_fence_after();
+      }
+      constexpr int NCH = 128 / C::CHUNK;  // staging rows' chunks of this warp's 128 columns
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int k0 = j.k0 + half * 128 + c * C::CHUNK;
+        uint32_t v[C::CHUNK];
+        if (j.kb > 0) {
+#pragma unroll
+          for (int h = 0; h < C::CHUNK / 32; ++h)
+            tmem_ld_32x32b_x32(tb + (uint32_t)(c * C::CHUNK + h * 32),
+                               *reinterpret_cast<uint32_t(*)[32]>(v + h * 32));
+          tmem_wait_ld();
+          if (c == NCH - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + acc.stage), 0));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::CHUNK; ++i) v[i] = 0u;
+        }
+        if (k0 >= p.k || n0 >= p.n) continue;
+        if (p.accumulate && n0 + lane < p.n) {
+          const TO *o = static_cast<const TO *>(p.dw) + ((size_t)j.g * p.n + n0 + lane) * p.k + k0;
+#pragma unroll
+          for (int i = 0; i < C::CHUNK; ++i)
+            if (k0 + i < p.k) v[i] = __float_as_uint(to_f(o[i]) + __uint_as_float(v[i]));
+        }
+        uint8_t *row = stg + buf * 4096 + lane * 128;
+        if (lane == 0) store_wait_read<1>();  // the store before the last has left this buffer
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 o;
+          if (sizeof(TO) == 4) {
+            o = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(
+                  __uint_as_float(v[(8 * i + 2 * e) % C::CHUNK]), __uint_as_float(v[(8 * i + 2 * e + 1) % C::CHUNK]));
+              w[e] = *reinterpret_cast<const uint32_t *>(&b2);
+            }
+            o = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          *reinterpret_cast<uint4 *>(row + ((i ^ (lane & 7)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          store_3d(&tmC, stg + buf * 4096, k0, n0, j.g);
+          store_commit();
+        }
+        buf ^= 1;
+      }
+      if (j.kb > 0) acc.next(2);
+    }
+    if (lane == 0) store_wait_all();
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    for (int s = 0; s < STAGES; ++s)
+      if (pending[s] >= 2) drain(tail + s, (uint32_t)(pending[s] - 2));
+    if (leader) {
+      for (int s = 0; s < STAGES; ++s)
+        if (pending[s] == 0 || pending[s] == 1) drain(full + s, (uint32_t)pending[s]);
+    } else {
+      pause_ns(200000);
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+}  // namespace tcg
+}  // namespace moe

@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "grouped.cuh"
 #include "grouped_simt.cuh"
+#include "grouped_tc.cuh"
 #include "moe_train.h"
 
 namespace moe {
@@ -100,15 +101,185 @@ simt::Args simt_args(const Product &p) {
   return a;
 }
 
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// ---------------------------------------------------------- tensor-core path
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
+// Row-major [planes, rows, cols] tensor (planes 0: a matrix), 128-byte
+// swizzled boxes of box_rows x 128 bytes; what lies outside reads as zero and
+// is not written.
+bool tensor_map(CUtensorMap *m, const void *base, moe_dtype dt, uint64_t planes, uint64_t rows,
+                uint64_t cols, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t e = elem(dt);
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {cols * e, rows * cols * e};
+  cuuint32_t box[3] = {(uint32_t)(128 / e), box_rows, 1};
+  cuuint32_t step[3] = {1, 1, 1};
+  return fn(m, dt == MOE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            planes ? 3 : 2, const_cast<void *>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One block, or one pair of blocks, per SM or SM pair.
+template <typename... A>
+moe_status launch_persistent(void (*kern)(A...), int threads, size_t smem, int cg, int64_t tiles,
+                             cudaStream_t s, A... args) {
+  if (smem > 232448) return MOE_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const int nsm = sm_count();
+  if (nsm < 2) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  int64_t units = nsm / cg;
+  if (cg == 2) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  if (cg == 2) {
+    // SM pairs that can be resident together, looked up once per kernel and device
+    static int resident[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    int n = dev < 64 ? resident[dev] : 0;
+    if (n == 0) {
+      cfg.gridDim = dim3((unsigned)(units * 2));
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();  // not sticky: the launch below decides
+        n = (int)units;
+      }
+      if (dev < 64) resident[dev] = n;
+    }
+    if (n < units) units = n;
+  }
+  if (tiles < units) units = tiles > 0 ? tiles : 1;
+  cfg.gridDim = dim3((unsigned)(units * cg));
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return MOE_ERR_CUDA;
+  return launch_status();
+}
+
+// Upper bound on the row tiles of all groups.
+int64_t row_tiles(const moe_grouped_shape *s, int bn) {
+  return s->rows / bn + (s->rows < s->groups ? s->rows : s->groups);
+}
+
+struct RowMaps {
+  CUtensorMap a0, a1, b0, b1;
+};
+
+// Maps of a product with rows x0 (and x1) [rows, contract] and weights w0
+// (and w1); `kmajor`: weights [G, F, contract], else [G, contract, F].
+template <typename C>
+bool row_maps(RowMaps *m, const moe_grouped_shape *s, const void *w0, const void *w1,
+              const void *x0, const void *x1, uint64_t F, uint64_t contract) {
+  auto wmap = [&](CUtensorMap *t, const void *w) {
+    return C::KMAJOR ? tensor_map(t, w, MOE_BF16, s->groups, F, contract, tcg::BM)
+                     : tensor_map(t, w, MOE_BF16, s->groups, contract, F, 64);
+  };
+  auto xmap = [&](CUtensorMap *t, const void *x) {
+    return tensor_map(t, x, MOE_BF16, 0, s->rows, contract, C::BOXN);
+  };
+  if (!wmap(&m->a0, w0) || !xmap(&m->b0, x0)) return false;
+  m->a1 = m->a0;
+  m->b1 = m->b0;
+  return (!w1 || wmap(&m->a1, w1)) && (!x1 || xmap(&m->b1, x1));
+}
+
+template <int OP, int CG, int AT, int BN, int STAGES, typename TO>
+moe_status launch_rows(const moe_grouped_shape *s, const void *w0, const void *w1, const void *x0,
+                       const void *x1, int F, int contract, tcg::RowParams p, cudaStream_t st) {
+  using C = tcg::RowCfg<OP, CG, AT, BN, STAGES>;
+  RowMaps m;
+  if (!row_maps<C>(&m, s, w0, w1, x0, x1, F, contract)) return MOE_ERR_CUDA;
+  p.G = s->groups;
+  p.F = F;
+  p.rows = s->rows;
+  p.kb0 = (contract + tcg::BK - 1) / tcg::BK;
+  p.kb = x1 ? 2 * p.kb0 : p.kb0;
+  const int64_t tiles = row_tiles(s, BN) * ((F + C::FEAT - 1) / C::FEAT);
+  return launch_persistent(tcg::rows_gemm<OP, CG, AT, BN, STAGES, TO>, C::NT, C::smem(p.G), CG, tiles,
+                           st, m.a0, m.a1, m.b0, m.b1, (const tcg::RowParams)p);
+}
+
+// rows of a group on average
+int64_t mean_rows(const moe_grouped_shape *s) { return (s->rows + s->groups - 1) / s->groups; }
+
+template <int OP, typename TO>
+moe_status tc_rows(const Product &p, int F, int contract) {
+  tcg::RowParams r = {};
+  r.offsets = p.offsets;
+  r.out = p.out;
+  r.status = p.status;
+  const auto *s = p.s;
+  if (mean_rows(s) <= 48)
+    return launch_rows<OP, 1, 1, 64, 8, TO>(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream);
+  if (F < 512)
+    return launch_rows<OP, 1, 1, 256, 4, TO>(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream);
+  return launch_rows<OP, 2, 2, 256, 4, TO>(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream);
+}
+
+template <typename TO>
+moe_status tc_dw(const Product &p) {
+  using C = tcg::DwCfg<TO>;
+  const auto *s = p.s;
+  CUtensorMap a, b, c;
+  if (!tensor_map(&a, p.a0, MOE_BF16, 0, s->rows, s->n, tcg::BK) ||
+      !tensor_map(&b, p.b0, MOE_BF16, 0, s->rows, s->k, tcg::BK) ||
+      !tensor_map(&c, p.out, p.out_dt, s->groups, s->n, s->k, 32))
+    return MOE_ERR_CUDA;
+  const tcg::DwParams d{p.offsets, s->groups, s->n, s->k, s->rows, p.out, p.accumulate, p.status};
+  const int64_t tiles = (int64_t)s->groups * ((s->n + 255) / 256) * ((s->k + 255) / 256);
+  return launch_persistent(tcg::dw_gemm<TO>, C::NT, C::smem(s->groups), 2, tiles, p.stream, a, b, c, d);
+}
+
+// Tensor maps need 16-byte aligned addresses and row pitches.
+bool tc_operand(const void *p, int64_t cols, moe_dtype dt) {
+  return aligned(p, 16) && cols * elem(dt) % 16 == 0;
+}
+
 moe_status run_linear(const Product &p) {
+  if (p.dt == MOE_BF16 && tc_operand(p.a0, p.s->k, p.dt) && tc_operand(p.b0, p.s->k, p.dt))
+    return p.out_dt == MOE_F32 ? tc_rows<tcg::LIN, float>(p, p.s->n, p.s->k)
+                               : tc_rows<tcg::LIN, bf16>(p, p.s->n, p.s->k);
   return simt_product<simt::LIN>(simt_args(p), p.dt, p.out_dt, p.stream);
 }
 
 moe_status run_dx(const Product &p) {
+  if (p.dt == MOE_BF16 && tc_operand(p.a0, p.s->n, p.dt) && tc_operand(p.b0, p.s->k, p.dt) &&
+      tc_operand(p.a1, p.s->n, p.dt) && tc_operand(p.b1, p.s->k, p.dt))
+    return p.out_dt == MOE_F32 ? tc_rows<tcg::DX, float>(p, p.s->k, p.s->n)
+                               : tc_rows<tcg::DX, bf16>(p, p.s->k, p.s->n);
   return simt_product<simt::DX>(simt_args(p), p.dt, p.out_dt, p.stream);
 }
 
 moe_status run_dw(const Product &p) {
+  // without rows there is nothing to map; the CUDA-core kernel writes the zeros
+  if (p.dt == MOE_BF16 && p.s->rows > 0 && tc_operand(p.a0, p.s->n, p.dt) &&
+      tc_operand(p.b0, p.s->k, p.dt) && tc_operand(p.out, p.s->k, p.out_dt))
+    return p.out_dt == MOE_F32 ? tc_dw<float>(p) : tc_dw<bf16>(p);
   return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
 }
 
@@ -117,8 +288,6 @@ unsigned row_grid(int64_t warps) {
   const int64_t most = 148 * 8;
   return (unsigned)(blocks < most ? blocks : most);
 }
-
-bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
 }  // namespace moe
