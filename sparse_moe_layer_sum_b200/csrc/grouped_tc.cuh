@@ -130,6 +130,18 @@ __device__ __forceinline__ void pause_ns(int64_t ns) {
   }
 }
 
+// Register split of the blocks with eight epilogue warps: the first four warps
+// (producer, MMA issuer, two idle) give theirs to the epilogue, which keeps
+// 128 sums per thread.  4 * 72 + 8 * 216 = 12 * 168, the count at launch.
+constexpr int REG_LAUNCH = 168, REG_LOW = 72, REG_HIGH = 216;
+static_assert(4 * REG_LOW + 8 * REG_HIGH == 12 * REG_LAUNCH, "register split");
+__device__ __forceinline__ void regs_low() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+}
+__device__ __forceinline__ void regs_high() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HIGH));
+}
+
 // A whole warp waits: lane 0 polls and tells the others, so that the lanes
 // cannot disagree about a wait that runs out.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
@@ -172,14 +184,22 @@ struct RowParams {
   float *part;        // BWD: [ceil(F / 32), rows] terms of dgate
 };
 
+// Depth after which a partial sum leaves tensor memory and is added to the
+// others in fp32 registers.  The tensor cores cut a sum off at 2^-24 of its
+// size with every 16-deep MMA, always towards zero: 8e-6 of the result after
+// 7168 values, 5e-7 after 512.  Results that are rounded to bf16 do not show
+// it; fp32 ones, and 8-bit codes next to a rounding border, do.
+constexpr int SEG = 512 / BK;
+
 // CG: SMs per tile.  AT: A tiles per SM (UP: one of w1 and the same rows of
 // w3; LIN, DX: two blocks of features, which halves the row bytes each weight
-// byte is paired with).  BN: rows of a tile.
-template <int OP, int CG, int AT, int BN, int STAGES>
+// byte is paired with).  BN: rows of a tile.  SEGS: sums in segments; the
+// registers of the epilogue hold 128 x 256 of them per SM.
+template <int OP, int CG, int AT, int BN, int STAGES, bool SEGS>
 struct RowCfg {
   static constexpr bool KMAJOR = OP == LIN || OP == UP;
   static constexpr int EPI = BN >= 128 ? 8 : 4;  // epilogue warps
-  static constexpr int NT = 32 * (2 + EPI);
+  static constexpr int NT = 32 * (4 + EPI);      // warps 2 and 3 idle
   static constexpr int BROWS = BN / CG;  // rows of the B tile in one SM
   static constexpr int BOXN = BROWS < 32 ? BROWS : 32;
   static constexpr int A_ALL = AT * TILE;
@@ -196,7 +216,10 @@ struct RowCfg {
   static size_t smem(int G) { return 1024 + TAB + Table::bytes(G); }
   static_assert(BROWS % BOXN == 0 && BOXN % 8 == 0, "row boxes");
   static_assert(NBUF * ACC <= 512, "tensor memory columns");
+  static constexpr int STEP = 32 * (EPI / 4);   // between a warp's 32-row chunks
+  static constexpr int NCH = BN / STEP;         // chunks of a warp and A tile
   static_assert(OP != UP || AT == 2, "UP pairs w1 and w3");
+  static_assert(!SEGS || (NBUF == 2 && AT * NCH <= 4), "sums in registers");
 };
 
 // The sum over the 32 lanes of each of 32 values; lane j returns value j's.
@@ -215,12 +238,105 @@ __device__ __forceinline__ float lane_sums(float (&v)[32]) {
   return v[0];
 }
 
-template <int OP, int CG, int AT, int BN, int STAGES, typename TO>
-__global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES>::NT, 1)
+// The result of one accumulator chunk: lane l holds feature fw + l of the 32
+// rows from row0 on, the first nv of which belong to the tile.
+
+template <typename TO>
+__device__ __forceinline__ void finish_rows(const RowParams &p, const float (&v)[32], int fw, int row0,
+                                            int nv) {
+  const int f = fw + threadIdx.x % 32;
+  if (f >= p.F) return;
+  TO *o = static_cast<TO *>(p.out) + (size_t)row0 * p.F + f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (j < nv) *o = from_f<TO>(v[j]);
+    o += p.F;
+  }
+}
+
+// A warp holds the 32 features of one scale block: the block's largest
+// magnitude is one warp reduction per row and projection.
+__device__ __forceinline__ void finish_up(const RowParams &p, const float (&va)[32],
+                                          const float (&vu)[32], int fw, int row0, int nv) {
+  const int lane = threadIdx.x % 32, f = fw + lane;
+  const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
+  size_t at = (size_t)row0 * p.F + f;
+  int ea = 0, eu = 0;  // lane j keeps row j's scales
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float a = va[j], u = vu[j];
+    const int ja = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(a)));
+    const int ju = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(u)));
+    if (lane == j) {
+      ea = ja;
+      eu = ju;
+    }
+    if (j < nv && f < p.F) {
+      static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(a * ckpt::sigmoid<bf16>(a) * u);
+      const uint16_t c = f32x2_to_e4m3x2(ckpt::scaled(a, ckpt::inv_scale_of(ja)),
+                                         ckpt::scaled(u, ckpt::inv_scale_of(ju)));
+      p.saved.ca[at] = (uint8_t)(c & 0xffu);
+      p.saved.cu[at] = (uint8_t)(c >> 8);
+    }
+    at += p.F;
+  }
+  if (lane < nv && fw < p.F) {
+    const size_t sat = (size_t)(row0 + lane) * nb + fw / ckpt::BLOCK;
+    p.saved.ea[sat] = (uint8_t)ea;
+    p.saved.eu[sat] = (uint8_t)eu;
+  }
+}
+
+// dh in, the gradients out; the chunk's terms of dgate are summed over the
+// warp's 32 features and left in `part`.
+__device__ __forceinline__ void finish_bwd(const RowParams &p, float (&v)[32], int fw, int row0,
+                                           int nv) {
+  const int lane = threadIdx.x % 32, f = fw + lane;
+  const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
+  if (fw >= p.F) return;
+  // lane j: the scales and the gate of row j
+  const bool mine = lane < nv;
+  const size_t sat = (size_t)(row0 + lane) * nb + fw / ckpt::BLOCK;
+  const int ea = mine ? p.saved.ea[sat] : 0, eu = mine ? p.saved.eu[sat] : 0;
+  const float gt = mine && p.gate ? p.gate[row0 + lane] : 1.0f;
+  const size_t at0 = (size_t)row0 * p.F + f;
+#pragma unroll
+  for (int j0 = 0; j0 < 32; j0 += 16) {
+    uint16_t q[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const bool on = j0 + j < nv && f < p.F;
+      const size_t at = at0 + (size_t)(j0 + j) * p.F;
+      q[j] = on ? (uint16_t)(__ldg(p.saved.ca + at) | __ldg(p.saved.cu + at) << 8) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int r = j0 + j;
+      const float2 d = ckpt::decode2(q[j]);
+      const float a = d.x * ckpt::scale_of(__shfl_sync(0xffffffffu, ea, r));
+      const float u = d.y * ckpt::scale_of(__shfl_sync(0xffffffffu, eu, r));
+      const float g = __shfl_sync(0xffffffffu, gt, r);
+      float xa, xu, xh;
+      const float s = ckpt::swiglu_grad<bf16>(a, u, v[r], g, xa, xu, xh);
+      v[r] = f < p.F ? s : 0.0f;
+      if (r < nv && f < p.F) {
+        const size_t at = at0 + (size_t)r * p.F;
+        p.da[at] = __float2bfloat16_rn(xa);
+        p.du[at] = __float2bfloat16_rn(xu);
+        p.hg[at] = __float2bfloat16_rn(xh);
+      }
+    }
+  }
+  const float sum = lane_sums(v);
+  if (mine) p.part[(size_t)(fw / ckpt::BLOCK) * p.rows + row0 + lane] = sum;
+}
+
+template <int OP, int CG, int AT, int BN, int STAGES, bool SEGS, typename TO>
+__global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
     rows_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
               const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
               const RowParams p) {
-  using C = RowCfg<OP, CG, AT, BN, STAGES>;
+  using C = RowCfg<OP, CG, AT, BN, STAGES, SEGS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = align_smem(smem_raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::BAR), *empty = full + STAGES;
@@ -269,6 +385,8 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES>::NT, 1)
   const uint32_t tmem = *tmem_slot;
   const int total = tab.start[p.G];
 
+  if (warp < 4) {
+    if (C::EPI == 8) regs_low();
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
@@ -327,15 +445,23 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES>::NT, 1)
       bool ok = true;
       for (int tile = unit; ok && tile < total; tile += nunits) {
         const Tile t = find_tile(tab, tile, p.G);
-        if (!wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc.stage * C::ACC);
         const uint32_t idesc =
             idesc_bf16_f32(BM * CG, (t.nvalid + 15) & ~15) | (C::KMAJOR ? 0u : A_MN);
+        uint32_t d = 0;
         for (int kb = 0; kb < p.kb; ++kb) {
+          const bool first = kb == 0 || (SEGS && kb % SEG == 0);
+          if (first) {
+            if (kb > 0) {
+              commit<CG>(accf + acc.stage);
+              acc.next(C::NBUF);
+            }
+            if (!wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d = tmem + (uint32_t)(acc.stage * C::ACC);
+          }
           if (!wait_bounded(full + r.stage, r.phase, abort_flag, WAIT_NS, p.status)) {
             ok = false;
             break;
@@ -350,7 +476,7 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES>::NT, 1)
             for (int i = 0; i < AT; ++i) {
               const uint64_t ad = C::KMAJOR ? sdesc_sw128(a + i * TILE + kk * 32)
                                             : desc_mn(a + i * TILE + kk * 2048);
-              mma<CG>(d + i * BN, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+              mma<CG>(d + i * BN, ad, bd, idesc, first && kk == 0 ? 0u : 1u);
             }
           }
           commit<CG>(empty + r.stage);
@@ -368,148 +494,94 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES>::NT, 1)
         drain(drained, 0);
       }
     }
+  }
   } else {
+    if (C::EPI == 8) regs_high();
     // -------------------------------------------------------------- epilogue
-    const int q = warp & 3;               // TMEM lane quarter of this warp
-    const int half = (warp - 2) >> 2;     // alternate 32-row chunks with 8 warps
-    constexpr int STEP = 32 * (C::EPI / 4);
-    const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
+    const int q = warp & 3;            // TMEM lane quarter of this warp
+    const int half = (warp - 4) >> 2;  // alternate 32-row chunks with 8 warps
+    constexpr int STEP = C::STEP, NCH = C::NCH;
     Ring acc;
+    uint32_t tb = 0;
+    auto acquire = [&]() {
+      if (!wait_warp(accf + acc.stage, acc.phase, abort_flag, p.status)) return false;
+      tc_fence_after();
+      tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.stage * C::ACC);
+      return true;
+    };
+    auto release = [&]() {  // hands the accumulator back to the MMA
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_cluster(mapa_shared(smem_u32(acce + acc.stage), 0));
+        else
+          mbar_arrive(acce + acc.stage);
+      }
+      acc.next(C::NBUF);
+    };
     for (int tile = unit; tile < total; tile += nunits) {
       const Tile t = find_tile(tab, tile, p.G);
-      if (!wait_warp(accf + acc.stage, acc.phase, abort_flag, p.status)) break;
-      tc_fence_after();
-      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.stage * C::ACC);
-      auto release = [&]() {  // hands the accumulator back to the MMA
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2)
-            mbar_arrive_cluster(mapa_shared(smem_u32(acce + acc.stage), 0));
-          else
-            mbar_arrive(acce + acc.stage);
-        }
-      };
-      // 32-row chunks of this warp
-      const int nch = t.nvalid > half * 32 ? (t.nvalid - half * 32 + STEP - 1) / STEP : 0;
       const int fw = t.ft * C::FEAT + (int)rank * BM + q * 32;  // the warp's first feature
-      if (OP == LIN || OP == DX) {
+      if (SEGS) {
+        // sum[a * NCH + ch]: chunk ch of A tile a
+        float sum[AT * NCH][32];
+        bool ok = true;
+        for (int kb = 0; kb < p.kb; kb += SEG) {
+          if (!(ok = acquire())) break;
+#pragma unroll
+          for (int i = 0; i < AT * NCH; ++i) {
+            const int c0 = half * 32 + i % NCH * STEP;
+            if (c0 >= t.nvalid) continue;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tb + (uint32_t)(i / NCH * BN + c0), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              sum[i][j] = kb == 0 ? __uint_as_float(v[j]) : sum[i][j] + __uint_as_float(v[j]);
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < (OP == UP ? 1 : AT) * NCH; ++i) {
+          const int c0 = half * 32 + i % NCH * STEP, fa = fw + i / NCH * BM * CG;
+          if (c0 >= t.nvalid) continue;
+          if (OP == UP)
+            finish_up(p, sum[i], sum[(AT - 1) * NCH + i], fa, t.row0 + c0, t.nvalid - c0);
+          else if (OP == BWD)
+            finish_bwd(p, sum[i], fa, t.row0 + c0, t.nvalid - c0);
+          else
+            finish_rows<TO>(p, sum[i], fa, t.row0 + c0, t.nvalid - c0);
+        }
+      } else {
         // chunks are read in batches; the accumulator goes back right after
         // the last batch's reads, so its stores overlap the next tile's MMAs
+        if (!acquire()) break;
         constexpr int NB = C::EPI == 8 ? 4 : 2;
+        const int nch = t.nvalid > half * 32 ? (t.nvalid - half * 32 + STEP - 1) / STEP : 0;
         const int nall = AT * nch;
+        const uint32_t t0 = tb;
         if (nall == 0) release();
         for (int i0 = 0; i0 < nall; i0 += NB) {
           uint32_t v[NB][32];
 #pragma unroll
           for (int u = 0; u < NB; ++u)
             if (i0 + u < nall)
-              tmem_ld_32x32b_x32(tb + (uint32_t)((i0 + u) / nch * BN + half * 32 + (i0 + u) % nch * STEP), v[u]);
+              tmem_ld_32x32b_x32(t0 + (uint32_t)((i0 + u) / nch * BN + half * 32 + (i0 + u) % nch * STEP), v[u]);
           tmem_wait_ld();
           if (i0 + NB >= nall) release();
 #pragma unroll
           for (int u = 0; u < NB; ++u)
             if (i0 + u < nall) {
-              const int f = fw + (i0 + u) / nch * BM * CG + lane;
               const int c0 = half * 32 + (i0 + u) % nch * STEP;
-              TO *o = static_cast<TO *>(p.out) + (size_t)(t.row0 + c0) * p.F + f;
-              if (f < p.F) {
+              float o[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (c0 + j < t.nvalid) o[(size_t)j * p.F] = from_f<TO>(__uint_as_float(v[u][j]));
-              }
+              for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(v[u][j]);
+              finish_rows<TO>(p, o, fw + (i0 + u) / nch * BM * CG, t.row0 + c0, t.nvalid - c0);
             }
         }
-      } else if (OP == UP) {
-        // a lane holds one hidden feature for 32 rows, the warp the 32
-        // features of one scale block: the block's largest magnitude is one
-        // warp reduction per row
-        const int f = fw + lane;
-        for (int ch = 0; ch < nch; ++ch) {
-          const int c0 = half * 32 + ch * STEP;
-          uint32_t va[32], vu[32];
-          tmem_ld_32x32b_x32(tb + (uint32_t)c0, va);
-          tmem_ld_32x32b_x32(tb + (uint32_t)(BN + c0), vu);
-          tmem_wait_ld();
-          if (ch + 1 == nch) release();
-          const size_t at0 = (size_t)(t.row0 + c0) * p.F + f;
-          int ea = 0, eu = 0;  // lane j keeps row j's scales
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float a = __uint_as_float(va[j]), u = __uint_as_float(vu[j]);
-            const int ja = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(a)));
-            const int ju = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(u)));
-            if (lane == j) {
-              ea = ja;
-              eu = ju;
-            }
-            if (c0 + j < t.nvalid && f < p.F) {
-              const size_t at = at0 + (size_t)j * p.F;
-              static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(a * ckpt::sigmoid<bf16>(a) * u);
-              const uint16_t c = f32x2_to_e4m3x2(ckpt::scaled(a, ckpt::inv_scale_of(ja)),
-                                                 ckpt::scaled(u, ckpt::inv_scale_of(ju)));
-              p.saved.ca[at] = (uint8_t)(c & 0xffu);
-              p.saved.cu[at] = (uint8_t)(c >> 8);
-            }
-          }
-          if (c0 + lane < t.nvalid && fw < p.F) {
-            const size_t at = (size_t)(t.row0 + c0 + lane) * nb + fw / ckpt::BLOCK;
-            p.saved.ea[at] = (uint8_t)ea;
-            p.saved.eu[at] = (uint8_t)eu;
-          }
-        }
-        if (nch == 0) release();
-      } else {  // BWD
-        for (int a = 0; a < AT; ++a) {
-          const int fa = fw + a * BM * CG, f = fa + lane;
-          for (int ch = 0; ch < nch; ++ch) {
-            const int c0 = half * 32 + ch * STEP;
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(tb + (uint32_t)(a * BN + c0), v);
-            // lane j: the scales and the gate of row j
-            const bool mine = c0 + lane < t.nvalid && fa < p.F;
-            const size_t sat = (size_t)(t.row0 + c0 + lane) * nb + fa / ckpt::BLOCK;
-            const int ea = mine ? p.saved.ea[sat] : 0, eu = mine ? p.saved.eu[sat] : 0;
-            const float gt = mine && p.gate ? p.gate[t.row0 + c0 + lane] : 1.0f;
-            const size_t at0 = (size_t)(t.row0 + c0) * p.F + f;
-            tmem_wait_ld();
-            if (a + 1 == AT && ch + 1 == nch) release();
-            float term[32];
-#pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 16) {
-              uint8_t qa[16], qu[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const bool on = c0 + j0 + j < t.nvalid && f < p.F;
-                const size_t at = at0 + (size_t)(j0 + j) * p.F;
-                qa[j] = on ? p.saved.ca[at] : 0;
-                qu[j] = on ? p.saved.cu[at] : 0;
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int r = j0 + j;
-                const float2 d = ckpt::decode2((uint16_t)(qa[j] | qu[j] << 8));
-                const float av = d.x * ckpt::scale_of(__shfl_sync(0xffffffffu, ea, r));
-                const float uv = d.y * ckpt::scale_of(__shfl_sync(0xffffffffu, eu, r));
-                const float g = __shfl_sync(0xffffffffu, gt, r);
-                float xa, xu, xh;
-                const float s = ckpt::swiglu_grad<bf16>(av, uv, __uint_as_float(v[r]), g, xa, xu, xh);
-                term[r] = f < p.F ? s : 0.0f;
-                if (c0 + r < t.nvalid && f < p.F) {
-                  const size_t at = at0 + (size_t)r * p.F;
-                  p.da[at] = __float2bfloat16_rn(xa);
-                  p.du[at] = __float2bfloat16_rn(xu);
-                  p.hg[at] = __float2bfloat16_rn(xh);
-                }
-              }
-            }
-            const float sum = lane_sums(term);
-            if (mine) p.part[(size_t)(fa / ckpt::BLOCK) * p.rows + t.row0 + c0 + lane] = sum;
-          }
-        }
-        if (nch == 0) release();
       }
-      acc.next(C::NBUF);
     }
   }
 
@@ -563,7 +635,8 @@ struct DwParams {
 // A tile of 256 features of dy (128 per SM of the pair) by 256 columns of x.
 template <typename TO>
 struct DwCfg {
-  static constexpr int BN = 256, STAGES = 4, EPI = 8, NT = 32 * (2 + EPI);
+  static constexpr int BN = 256, STAGES = 4, EPI = 8, NT = 32 * (4 + EPI);
+  static constexpr bool SEGS = sizeof(TO) == 4;  // sums in segments (see SEG)
   static constexpr int STAGE = TILE + BN / 2 * BK * 2;  // per SM: 128 + 128 columns
   static constexpr int CHUNK = 128 / (int)sizeof(TO);   // columns of a 128-byte staging row
   static constexpr int STG = STAGES * STAGE;            // two 32 x 128-byte buffers per warp
@@ -644,6 +717,8 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
     return j;
   };
 
+  if (warp < 4) {
+    regs_low();
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
@@ -692,17 +767,23 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
     for (int64_t tile = unit; ok && tile < total; tile += nunits) {
       const Job j = job(tile);
       if (j.kb == 0) continue;
-      if (leader) {
-        if (!wait_warp(acce + acc.stage, acc.phase ^ 1u, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-      }
-      const uint32_t d = tmem + (uint32_t)(acc.stage * 256);
       const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
+      uint32_t d = 0;
       for (int i = 0; i < j.kb; ++i) {
         uint8_t *st = sm + r.stage * C::STAGE;
+        const bool first = i == 0 || (C::SEGS && i % SEG == 0);
+        if (leader && first) {
+          if (i > 0) {
+            if (lane == 0) commit<2>(accf + acc.stage);
+            acc.next(2);
+          }
+          if (!wait_warp(acce + acc.stage, acc.phase ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          d = tmem + (uint32_t)(acc.stage * 256);
+        }
         const bool fix = i == j.kb - 1 && j.tail % 16 != 0;
         // the SM that issues no MMAs follows the ring on its `tail` barriers
         if ((fix || !leader) && !wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
@@ -736,7 +817,7 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
             const uint32_t a = smem_u32(st), b = a + TILE;
             const int steps = i == j.kb - 1 ? (j.tail + 15) / 16 : BK / 16;
             for (int s = 0; s < steps; ++s)
-              mma<2>(d, desc_mn(a + s * 2048), desc_mn(b + s * 2048), idesc, (i | s) != 0 ? 1u : 0u);
+              mma<2>(d, desc_mn(a + s * 2048), desc_mn(b + s * 2048), idesc, first && s == 0 ? 0u : 1u);
             commit<2>(empty + r.stage);
           }
           __syncwarp();
@@ -753,67 +834,58 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
       drain(drained, 0);
     }
     __syncwarp();
+  }
   } else {
+    regs_high();
     // -------------------------------------------------------------- epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t *stg = sm + C::STG + (warp - 2) * 2 * 4096;
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    constexpr int CH = C::CHUNK, NCH = 128 / CH;  // this warp's 128 columns in chunks
+    uint8_t *stg = sm + C::STG + (warp - 4) * 2 * 4096;
     int buf = 0;
     Ring acc;
+    uint32_t tb = 0;
+    auto acquire = [&]() {
+      if (!wait_warp(accf + acc.stage, acc.phase, abort_flag, p.status)) return false;
+      tc_fence_after();
+      tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.stage * 256 + half * 128);
+      return true;
+    };
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + acc.stage), 0));
+      acc.next(2);
+    };
     for (int64_t tile = unit; tile < total; tile += nunits) {
       const Job j = job(tile);
       if (j.kb == 0 && p.accumulate) continue;
       const int n0 = j.n0 + (int)rank * BM + q * 32;
-      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.stage * 256 + half * 128);
-      if (j.kb > 0) {
-        if (!wait_warp(accf + acc.stage, acc.phase, abort_flag, p.status)) break;
-        tc_fence_after();
-      }
-      constexpr int NCH = 128 / C::CHUNK;  // staging rows' chunks of this warp's 128 columns
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int k0 = j.k0 + half * 128 + c * C::CHUNK;
-        uint32_t v[C::CHUNK];
-        if (j.kb > 0) {
-#pragma unroll
-          for (int h = 0; h < C::CHUNK / 32; ++h)
-            tmem_ld_32x32b_x32(tb + (uint32_t)(c * C::CHUNK + h * 32),
-                               *reinterpret_cast<uint32_t(*)[32]>(v + h * 32));
-          tmem_wait_ld();
-          if (c == NCH - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + acc.stage), 0));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < C::CHUNK; ++i) v[i] = 0u;
-        }
-        if (k0 >= p.k || n0 >= p.n) continue;
+      // lane l stores columns k0 .. k0 + CH - 1 of feature n0 + l
+      auto emit = [&](float (&v)[CH], int c) {
+        const int k0 = j.k0 + half * 128 + c * CH;
+        if (k0 >= p.k || n0 >= p.n) return;
         if (p.accumulate && n0 + lane < p.n) {
           const TO *o = static_cast<const TO *>(p.dw) + ((size_t)j.g * p.n + n0 + lane) * p.k + k0;
 #pragma unroll
-          for (int i = 0; i < C::CHUNK; ++i)
-            if (k0 + i < p.k) v[i] = __float_as_uint(to_f(o[i]) + __uint_as_float(v[i]));
+          for (int i = 0; i < CH; ++i)
+            if (k0 + i < p.k) v[i] += to_f(o[i]);
         }
         uint8_t *row = stg + buf * 4096 + lane * 128;
         if (lane == 0) store_wait_read<1>();  // the store before the last has left this buffer
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          uint4 o;
-          if (sizeof(TO) == 4) {
-            o = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else {
-            uint32_t w[4];
+          uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(
-                  __uint_as_float(v[(8 * i + 2 * e) % C::CHUNK]), __uint_as_float(v[(8 * i + 2 * e + 1) % C::CHUNK]));
+          for (int e = 0; e < 4; ++e) {
+            if (sizeof(TO) == 4) {
+              w[e] = __float_as_uint(v[(4 * i + e) % CH]);
+            } else {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[(8 * i + 2 * e) % CH], v[(8 * i + 2 * e + 1) % CH]);
               w[e] = *reinterpret_cast<const uint32_t *>(&b2);
             }
-            o = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *reinterpret_cast<uint4 *>(row + ((i ^ (lane & 7)) << 4)) = o;
+          *reinterpret_cast<uint4 *>(row + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -822,8 +894,47 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
           store_commit();
         }
         buf ^= 1;
+      };
+      if (C::SEGS || j.kb == 0) {
+        float sum[NCH][CH];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int i = 0; i < CH; ++i) sum[c][i] = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < j.kb; i += SEG) {
+          if (!(ok = acquire())) break;
+#pragma unroll
+          for (int c = 0; c < NCH * CH / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tb + (uint32_t)(c * 32), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sum[c * 32 / CH][c * 32 % CH + e] += __uint_as_float(v[e]);
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) emit(sum[c], c);
+      } else {
+        if (!acquire()) break;
+        const uint32_t t0 = tb;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+          float o[CH];
+#pragma unroll
+          for (int h = 0; h < CH / 32; ++h) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(t0 + (uint32_t)(c * CH + h * 32), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[h * 32 + e] = __uint_as_float(v[e]);
+          }
+          if (c == NCH - 1) release();
+          emit(o, c);
+        }
       }
-      if (j.kb > 0) acc.next(2);
     }
     if (lane == 0) store_wait_all();
   }

@@ -208,10 +208,10 @@ bool row_maps(RowMaps *m, const moe_grouped_shape *s, const void *w0, const void
   return (!w1 || wmap(&m->a1, w1)) && (!x1 || xmap(&m->b1, x1));
 }
 
-template <int OP, int CG, int AT, int BN, int STAGES, typename TO>
+template <int OP, int CG, int AT, int BN, int STAGES, bool SEGS, typename TO>
 moe_status launch_rows(const moe_grouped_shape *s, const void *w0, const void *w1, const void *x0,
                        const void *x1, int F, int contract, tcg::RowParams p, cudaStream_t st) {
-  using C = tcg::RowCfg<OP, CG, AT, BN, STAGES>;
+  using C = tcg::RowCfg<OP, CG, AT, BN, STAGES, SEGS>;
   RowMaps m;
   if (!row_maps<C>(&m, s, w0, w1, x0, x1, F, contract)) return MOE_ERR_CUDA;
   p.G = s->groups;
@@ -220,7 +220,7 @@ moe_status launch_rows(const moe_grouped_shape *s, const void *w0, const void *w
   p.kb0 = (contract + tcg::BK - 1) / tcg::BK;
   p.kb = x1 ? 2 * p.kb0 : p.kb0;
   const int64_t tiles = row_tiles(s, BN) * ((F + C::FEAT - 1) / C::FEAT);
-  return launch_persistent(tcg::rows_gemm<OP, CG, AT, BN, STAGES, TO>, C::NT, C::smem(p.G), CG, tiles,
+  return launch_persistent(tcg::rows_gemm<OP, CG, AT, BN, STAGES, SEGS, TO>, C::NT, C::smem(p.G), CG, tiles,
                            st, m.a0, m.a1, m.b0, m.b1, (const tcg::RowParams)p);
 }
 
@@ -234,11 +234,31 @@ moe_status tc_rows(const Product &p, int F, int contract) {
   r.out = p.out;
   r.status = p.status;
   const auto *s = p.s;
-  if (mean_rows(s) <= 48)
-    return launch_rows<OP, 1, 1, 64, 8, TO>(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream);
-  if (F < 512)
-    return launch_rows<OP, 1, 1, 256, 4, TO>(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream);
-  return launch_rows<OP, 2, 2, 256, 4, TO>(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream);
+  auto run = [&](auto launch) { return launch(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream); };
+  if constexpr (sizeof(TO) == 4) {  // fp32 results: sums in segments
+    if (mean_rows(s) <= 48 || F < 256) return run(launch_rows<OP, 1, 1, 64, 8, true, TO>);
+    return run(launch_rows<OP, 2, 1, 256, 6, true, TO>);
+  } else {
+    if (mean_rows(s) <= 48) return run(launch_rows<OP, 1, 1, 64, 8, false, TO>);
+    if (F < 512) return run(launch_rows<OP, 1, 1, 256, 4, false, TO>);
+    return run(launch_rows<OP, 2, 2, 256, 4, false, TO>);
+  }
+}
+
+// The first matmul with its checkpoint (n hidden features from k), and the
+// gradients of the hidden rows (contracting over k).
+moe_status tc_up(const moe_grouped_shape *s, const void *x, const void *w1, const void *w3,
+                 const tcg::RowParams &r, cudaStream_t st) {
+  if (mean_rows(s) <= 48 || s->n < 256)
+    return launch_rows<tcg::UP, 1, 2, 64, 5, true, bf16>(s, w1, w3, x, nullptr, s->n, s->k, r, st);
+  return launch_rows<tcg::UP, 2, 2, 128, 5, true, bf16>(s, w1, w3, x, nullptr, s->n, s->k, r, st);
+}
+
+moe_status tc_bwd(const moe_grouped_shape *s, const void *dy, const void *w2,
+                  const tcg::RowParams &r, cudaStream_t st) {
+  if (mean_rows(s) <= 48 || s->n < 256)
+    return launch_rows<tcg::BWD, 1, 1, 64, 8, true, bf16>(s, w2, nullptr, dy, nullptr, s->n, s->k, r, st);
+  return launch_rows<tcg::BWD, 2, 1, 256, 6, true, bf16>(s, w2, nullptr, dy, nullptr, s->n, s->k, r, st);
 }
 
 template <typename TO>
@@ -391,7 +411,7 @@ MOE_EXPORT moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps
 
 MOE_EXPORT size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
-  // the two projections in fp32
+  // the two projections in fp32, for the CUDA cores
   return 2 * align_up((size_t)s->rows * s->n * 4, 256);
 }
 
@@ -409,13 +429,21 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
     return MOE_ERR_INVALID;
   if (!ws || ws_bytes < moe_swiglu_checkpoint_workspace_size(s, dt)) return MOE_ERR_WORKSPACE;
   cudaStream_t cs = as_stream(stream);
+  const ckpt::Saved sv{codes_a, exps_a, codes_u, exps_u};
+  if (dt == MOE_BF16 && tc_operand(x, s->k, dt) && tc_operand(w1, s->k, dt) && tc_operand(w3, s->k, dt)) {
+    tcg::RowParams r = {};
+    r.offsets = offsets;
+    r.out = h;
+    r.status = dev_status;
+    r.saved = sv;
+    return tc_up(s, x, w1, w3, r, cs);
+  }
   float *a = static_cast<float *>(ws);
   float *u = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + align_up((size_t)s->rows * s->n * 4, 256));
   if ((st = run_linear({s, dt, MOE_F32, x, w1, nullptr, nullptr, offsets, a, 0, dev_status, cs})) != MOE_OK)
     return st;
   if ((st = run_linear({s, dt, MOE_F32, x, w3, nullptr, nullptr, offsets, u, 0, dev_status, cs})) != MOE_OK)
     return st;
-  const ckpt::Saved sv{codes_a, exps_a, codes_u, exps_u};
   const unsigned grid = row_grid(s->rows * ((s->n + ckpt::BLOCK - 1) / ckpt::BLOCK));
   if (dt == MOE_F32)
     ckpt::swiglu_save<<<grid, ckpt::ROW_THREADS, 0, cs>>>(a, u, offsets, s->groups, s->rows, s->n, static_cast<float *>(h), sv);
@@ -426,7 +454,9 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
 
 MOE_EXPORT size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
-  return align_up((size_t)s->rows * s->n * 4, 256);  // dh in fp32
+  // dh in fp32 for the CUDA cores; the tensor-core path keeps one term of
+  // dgate for 32 of its values
+  return align_up((size_t)s->rows * s->n * 4, 256);
 }
 
 MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
@@ -445,13 +475,28 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
     return MOE_ERR_INVALID;
   if (!ws || ws_bytes < moe_swiglu_backward_workspace_size(s, dt)) return MOE_ERR_WORKSPACE;
   cudaStream_t cs = as_stream(stream);
+  const ckpt::Saved sv{const_cast<uint8_t *>(codes_a), const_cast<uint8_t *>(exps_a),
+                       const_cast<uint8_t *>(codes_u), const_cast<uint8_t *>(exps_u)};
+  if (dt == MOE_BF16 && tc_operand(dy, s->k, dt) && tc_operand(w2, s->n, dt)) {
+    tcg::RowParams r = {};
+    r.offsets = offsets;
+    r.status = dev_status;
+    r.saved = sv;
+    r.gate = gate;
+    r.da = static_cast<bf16 *>(da);
+    r.du = static_cast<bf16 *>(du);
+    r.hg = static_cast<bf16 *>(hg);
+    r.part = static_cast<float *>(ws);
+    if ((st = tc_bwd(s, dy, w2, r, cs)) != MOE_OK) return st;
+    tcg::sum_parts<<<(unsigned)((s->rows + 255) / 256), 256, 0, cs>>>(
+        r.part, offsets, s->groups, s->rows, (s->n + ckpt::BLOCK - 1) / ckpt::BLOCK, dgate);
+    return launch_status();
+  }
   float *dh = static_cast<float *>(ws);
   // dh = dy w2: the input gradient of a linear layer from n features to k
   const moe_grouped_shape lin{s->groups, s->k, s->n, s->rows};
   if ((st = run_dx({&lin, dt, MOE_F32, dy, w2, nullptr, nullptr, offsets, dh, 0, dev_status, cs})) != MOE_OK)
     return st;
-  const ckpt::Saved sv{const_cast<uint8_t *>(codes_a), const_cast<uint8_t *>(exps_a),
-                       const_cast<uint8_t *>(codes_u), const_cast<uint8_t *>(exps_u)};
   const unsigned grid = row_grid(s->rows * (ckpt::ROW_THREADS / 32));
   if (dt == MOE_F32)
     ckpt::swiglu_grads<<<grid, ckpt::ROW_THREADS, 0, cs>>>(
