@@ -151,6 +151,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {  // bf16x2, rounded to nearest
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+
 struct Ring {  // position in a ring of stages
   int stage = 0;
   uint32_t phase = 0;
@@ -632,26 +637,31 @@ struct DwParams {
   int32_t *status;
 };
 
-// A tile of 256 features of dy (128 per SM of the pair) by 256 columns of x.
-template <typename TO>
+// A tile of AT * 256 features of dy (AT blocks of 128 per SM of the pair) by
+// 256 columns of x.
+template <typename TO, int AT>
 struct DwCfg {
-  static constexpr int BN = 256, STAGES = 4, EPI = 8, NT = 32 * (4 + EPI);
+  static constexpr int EPI = 8, NT = 32 * (4 + EPI);
   static constexpr bool SEGS = sizeof(TO) == 4;  // sums in segments (see SEG)
-  static constexpr int STAGE = TILE + BN / 2 * BK * 2;  // per SM: 128 + 128 columns
-  static constexpr int CHUNK = 128 / (int)sizeof(TO);   // columns of a 128-byte staging row
-  static constexpr int STG = STAGES * STAGE;            // two 32 x 128-byte buffers per warp
-  static constexpr int BAR = STG + EPI * 2 * 4096;
+  static constexpr int FEAT = AT * 256;
+  static constexpr int STAGE = AT * TILE + 128 * BK * 2;  // per SM: AT * 128 + 128 columns
+  static constexpr int STAGES = AT == 2 ? 4 : 6;          // 192 KB in flight
+  static constexpr int NBUF = 2 / AT;                     // accumulators of AT * 256 columns
+  static constexpr int CHUNK = 128 / (int)sizeof(TO);     // columns of a 128-byte staging row
+  static constexpr int STG = STAGES * STAGE;              // a 32 x 128-byte buffer per warp
+  static constexpr int BAR = STG + EPI * 4096;
   static constexpr int NBARS = 3 * STAGES + 5;
   static constexpr int MISC = BAR + NBARS * 8;
-  static constexpr int TAB = (MISC + 16 + 4 * STAGES + 15) / 16 * 16;
-  static size_t smem(int G) { return 1024 + TAB + Table::bytes(G); }
+  static constexpr int BYTES = 1024 + MISC + 16 + 4 * STAGES;
+  static_assert(!SEGS || AT == 1, "sums in registers");
+  static_assert(BYTES <= 232448, "shared memory");
 };
 
-template <typename TO>
-__global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
+template <typename TO, int AT>
+__global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     dw_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmC, const DwParams p) {
-  using C = DwCfg<TO>;
+  using C = DwCfg<TO, AT>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = align_smem(smem_raw);
@@ -661,7 +671,6 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 4);
   // per stage: -1, or the phase its copies complete, + 2 when they count on `tail`
   volatile int *pending = reinterpret_cast<volatile int *>(sm + C::MISC + 16);
-  const Table tab(sm + C::TAB, p.G);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -690,27 +699,27 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
-  build_table(tab, p.offsets, p.G, p.rows, 256, 1, p.status);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int ntiles = (p.n + 255) / 256, ktiles = (p.k + 255) / 256;
+  const int ntiles = (p.n + C::FEAT - 1) / C::FEAT, ktiles = (p.k + 255) / 256;
   const int64_t total = (int64_t)p.G * ntiles * ktiles;
 
   struct Job {
     int g, n0, k0, lo, kc, kb, tail;  // kb: k-blocks; tail: rows of the last one
     int nmma;                         // columns of the MMA
+    // whether k-block i ends inside a 16-row step
+    __device__ __forceinline__ bool fix(int i) const { return i == kb - 1 && tail % 16 != 0; }
   };
   auto job = [&](int64_t tile) {
     Job j;
     j.g = (int)(tile / (ntiles * ktiles));
     const int local = (int)(tile - (int64_t)j.g * ntiles * ktiles);
-    j.n0 = local / ktiles * 256;
+    j.n0 = local / ktiles * C::FEAT;
     j.k0 = local % ktiles * 256;
-    j.lo = tab.lo[j.g];
-    j.kc = tab.n[j.g];
+    group_bounds(p.offsets, j.g, p.rows, j.lo, j.kc, threadIdx.x == 0 ? p.status : nullptr);
     j.kb = (j.kc + BK - 1) / BK;
     j.tail = j.kc - (j.kb - 1) * BK;
     j.nmma = min(256, (p.k - j.k0 + 31) / 32 * 32);
@@ -722,14 +731,14 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
-      const uint64_t pol = policy_evict_last();  // rows are read by every tile of their group
+      const uint64_t pol = policy_evict_normal();
       Ring r;
       bool ok = true;
       for (int64_t tile = unit; ok && tile < total; tile += nunits) {
         const Job j = job(tile);
         const int hb = j.nmma / 2, nbox = (hb + 63) / 64;
         const int n0 = j.n0 + (int)rank * BM, k0 = j.k0 + (int)rank * hb;
-        const uint32_t bytes = (uint32_t)(TILE + nbox * BOX);
+        const uint32_t bytes = (uint32_t)(AT * TILE + nbox * BOX);
         for (int i = 0; i < j.kb; ++i) {
           if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
             ok = false;
@@ -737,7 +746,7 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
           }
           // a last block that ends inside a 16-row step is completed on each
           // SM's own `tail` barrier and handed on when its rows are zeroed
-          const bool fix = i == j.kb - 1 && j.tail % 16 != 0;
+          const bool fix = j.fix(i);
           uint32_t bar;
           if (fix) {
             mbar_arrive_expect_tx(tail + r.stage, bytes);
@@ -751,10 +760,11 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
             bar = mapa_shared(smem_u32(full + r.stage), 0);
           }
           pending[r.stage] = (int)r.phase + (fix ? 2 : 0);
-          uint8_t *a = sm + r.stage * C::STAGE, *b = a + TILE;
+          uint8_t *a = sm + r.stage * C::STAGE, *b = a + AT * TILE;
           const int row = j.lo + i * BK;
-          load_2d<2>(&tmA, a, bar, n0, row, pol);
-          load_2d<2>(&tmA, a + BOX, bar, n0 + 64, row, pol);
+#pragma unroll
+          for (int c = 0; c < 2 * AT; ++c)
+            load_2d<2>(&tmA, a + c * BOX, bar, n0 + c / 2 * 256 + c % 2 * 64, row, pol);
           for (int c = 0; c < nbox; ++c) load_2d<2>(&tmB, b + c * BOX, bar, k0 + c * 64, row, pol);
           r.next(STAGES);
         }
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
         if (leader && first) {
           if (i > 0) {
             if (lane == 0) commit<2>(accf + acc.stage);
-            acc.next(2);
+            acc.next(C::NBUF);
           }
           if (!wait_warp(acce + acc.stage, acc.phase ^ 1u, abort_flag, p.status)) {
             ok = false;
@@ -784,7 +794,7 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
           tc_fence_after();
           d = tmem + (uint32_t)(acc.stage * 256);
         }
-        const bool fix = i == j.kb - 1 && j.tail % 16 != 0;
+        const bool fix = j.fix(i);
         // the SM that issues no MMAs follows the ring on its `tail` barriers
         if ((fix || !leader) && !wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
           ok = false;
@@ -793,7 +803,7 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
         if (fix) {
           // rows tail .. next multiple of 16 of every 64-column box: 128
           // bytes each, whole rows, so the swizzle does not matter
-          const int nz = 16 - j.tail % 16, nbox = 2 + (j.nmma / 2 + 63) / 64;
+          const int nz = 16 - j.tail % 16, nbox = 2 * AT + (j.nmma / 2 + 63) / 64;
           for (int z = lane; z < nbox * nz * 8; z += 32) {
             const int bx = z / (nz * 8), w = z % (nz * 8);
             *reinterpret_cast<uint4 *>(st + bx * BOX + (j.tail + w / 8) * 128 + w % 8 * 16) =
@@ -814,10 +824,13 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
           tc_fence_after();
           if (lane == 0) {
             pending[r.stage] = -1;
-            const uint32_t a = smem_u32(st), b = a + TILE;
+            const uint32_t a = smem_u32(st), b = a + AT * TILE;
             const int steps = i == j.kb - 1 ? (j.tail + 15) / 16 : BK / 16;
             for (int s = 0; s < steps; ++s)
-              mma<2>(d, desc_mn(a + s * 2048), desc_mn(b + s * 2048), idesc, first && s == 0 ? 0u : 1u);
+#pragma unroll
+              for (int c = 0; c < AT; ++c)
+                mma<2>(d + c * 256, desc_mn(a + c * TILE + s * 2048), desc_mn(b + s * 2048), idesc,
+                       first && s == 0 ? 0u : 1u);
             commit<2>(empty + r.stage);
           }
           __syncwarp();
@@ -827,7 +840,7 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
       if (!ok) break;
       if (leader && lane == 0) commit<2>(accf + acc.stage);
       __syncwarp();
-      acc.next(2);
+      acc.next(C::NBUF);
     }
     if (!ok && leader && lane == 0) {
       mma_commit_pair(drained);
@@ -840,8 +853,7 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, half = (warp - 4) >> 2;
     constexpr int CH = C::CHUNK, NCH = 128 / CH;  // this warp's 128 columns in chunks
-    uint8_t *stg = sm + C::STG + (warp - 4) * 2 * 4096;
-    int buf = 0;
+    uint8_t *stg = sm + C::STG + (warp - 4) * 4096;
     Ring acc;
     uint32_t tb = 0;
     auto acquire = [&]() {
@@ -854,15 +866,29 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acce + acc.stage), 0));
-      acc.next(2);
+      acc.next(C::NBUF);
     };
     for (int64_t tile = unit; tile < total; tile += nunits) {
       const Job j = job(tile);
       if (j.kb == 0 && p.accumulate) continue;
-      const int n0 = j.n0 + (int)rank * BM + q * 32;
-      // lane l stores columns k0 .. k0 + CH - 1 of feature n0 + l
+      // lane l stores columns k0 .. k0 + CH - 1 of feature n0 + l; `word(i)`
+      // is the i-th 4-byte word of its row of the staging buffer
+      auto store = [&](int n0, int k0, auto word) {
+        if (lane == 0) store_wait_read<0>();  // the last store has left the buffer
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4 *>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_uint4(word(4 * i), word(4 * i + 1), word(4 * i + 2), word(4 * i + 3));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          store_3d(&tmC, stg, k0, n0, j.g);
+          store_commit();
+        }
+      };
       auto emit = [&](float (&v)[CH], int c) {
-        const int k0 = j.k0 + half * 128 + c * CH;
+        const int n0 = j.n0 + (int)rank * BM + q * 32, k0 = j.k0 + half * 128 + c * CH;
         if (k0 >= p.k || n0 >= p.n) return;
         if (p.accumulate && n0 + lane < p.n) {
           const TO *o = static_cast<const TO *>(p.dw) + ((size_t)j.g * p.n + n0 + lane) * p.k + k0;
@@ -870,31 +896,42 @@ __global__ void __launch_bounds__(DwCfg<TO>::NT, 1)
           for (int i = 0; i < CH; ++i)
             if (k0 + i < p.k) v[i] += to_f(o[i]);
         }
-        uint8_t *row = stg + buf * 4096 + lane * 128;
-        if (lane == 0) store_wait_read<1>();  // the store before the last has left this buffer
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (sizeof(TO) == 4) {
-              w[e] = __float_as_uint(v[(4 * i + e) % CH]);
-            } else {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[(8 * i + 2 * e) % CH], v[(8 * i + 2 * e + 1) % CH]);
-              w[e] = *reinterpret_cast<const uint32_t *>(&b2);
-            }
-          }
-          *reinterpret_cast<uint4 *>(row + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          store_3d(&tmC, stg + buf * 4096, k0, n0, j.g);
-          store_commit();
-        }
-        buf ^= 1;
+        store(n0, k0, [&](int i) {
+          if (sizeof(TO) == 4) return __float_as_uint(v[i % CH]);
+          return pack(v[2 * i % CH], v[(2 * i + 1) % CH]);
+        });
       };
+      if constexpr (AT == 2) {
+        // one accumulator: it is read out as packed bf16 (128 registers) and
+        // handed back before any of it is stored
+        uint32_t w[2][64];
+        if (j.kb > 0) {
+          if (!acquire()) break;
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(tb + (uint32_t)(a * 256 + c * 32), v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                w[a][c * 16 + e] = pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+            }
+          release();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) w[0][i] = w[1][i] = 0u;
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            const int n0 = j.n0 + a * 256 + (int)rank * BM + q * 32, k0 = j.k0 + half * 128 + c * CH;
+            if (n0 < p.n && k0 < p.k) store(n0, k0, [&](int i) { return w[a][c * 32 + i]; });
+          }
+        continue;
+      }
       if (C::SEGS || j.kb == 0) {
         float sum[NCH][CH];
 #pragma unroll

@@ -261,9 +261,9 @@ moe_status tc_bwd(const moe_grouped_shape *s, const void *dy, const void *w2,
   return launch_rows<tcg::BWD, 2, 1, 256, 6, true, bf16>(s, w2, nullptr, dy, nullptr, s->n, s->k, r, st);
 }
 
-template <typename TO>
-moe_status tc_dw(const Product &p) {
-  using C = tcg::DwCfg<TO>;
+template <typename TO, int AT>
+moe_status launch_dw(const Product &p) {
+  using C = tcg::DwCfg<TO, AT>;
   const auto *s = p.s;
   CUtensorMap a, b, c;
   if (!tensor_map(&a, p.a0, MOE_BF16, 0, s->rows, s->n, tcg::BK) ||
@@ -271,8 +271,16 @@ moe_status tc_dw(const Product &p) {
       !tensor_map(&c, p.out, p.out_dt, s->groups, s->n, s->k, 32))
     return MOE_ERR_CUDA;
   const tcg::DwParams d{p.offsets, s->groups, s->n, s->k, s->rows, p.out, p.accumulate, p.status};
-  const int64_t tiles = (int64_t)s->groups * ((s->n + 255) / 256) * ((s->k + 255) / 256);
-  return launch_persistent(tcg::dw_gemm<TO>, C::NT, C::smem(s->groups), 2, tiles, p.stream, a, b, c, d);
+  const int64_t tiles = (int64_t)s->groups * ((s->n + C::FEAT - 1) / C::FEAT) * ((s->k + 255) / 256);
+  return launch_persistent(tcg::dw_gemm<TO, AT>, C::NT, (size_t)C::BYTES, 2, tiles, p.stream, a, b, c, d);
+}
+
+moe_status tc_dw(const Product &p) {
+  if (p.out_dt == MOE_F32) return launch_dw<float, 1>(p);
+  // a bf16 sum with what is there already adds in fp32, which the packed
+  // results of the wider tile no longer are
+  if (p.accumulate || p.s->n <= 256) return launch_dw<bf16, 1>(p);
+  return launch_dw<bf16, 2>(p);
 }
 
 // Tensor maps need 16-byte aligned addresses and row pitches.
@@ -299,7 +307,7 @@ moe_status run_dw(const Product &p) {
   // without rows there is nothing to map; the CUDA-core kernel writes the zeros
   if (p.dt == MOE_BF16 && p.s->rows > 0 && tc_operand(p.a0, p.s->n, p.dt) &&
       tc_operand(p.b0, p.s->k, p.dt) && tc_operand(p.out, p.s->k, p.out_dt))
-    return p.out_dt == MOE_F32 ? tc_dw<float>(p) : tc_dw<bf16>(p);
+    return tc_dw(p);
   return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
 }
 
