@@ -27,21 +27,18 @@ __device__ __forceinline__ void group_bounds(const int32_t *__restrict__ off, in
   n = (int)(cb - ca);
 }
 
-// Group g's n rows are cut into ntt tiles of `base` rows (a multiple of 16,
-// at most rows_max); each token tile meets ft feature tiles.  start is the
-// exclusive prefix of ntt * ft; start[G] the number of tiles.
+// Group g's rows are lo[g] .. lo[g + 1] - 1 (none where that runs backwards).
+// They are cut into ntt tiles of `base` rows, a multiple of 16 and at most
+// rows_max; each token tile meets ft feature tiles.  start is the exclusive
+// prefix of ntt * ft over the groups; start[G] the number of tiles.
 struct Table {
   int32_t *start;  // [G + 1]
-  int32_t *base;   // [G]
-  int32_t *lo;     // [G]
-  int32_t *n;      // [G]
-  static size_t bytes(int G) { return sizeof(int32_t) * (size_t)(4 * G + 1); }
-  __device__ __forceinline__ Table(void *mem, int G) {
-    start = static_cast<int32_t *>(mem);
-    base = start + G + 1;
-    lo = base + G;
-    n = lo + G;
-  }
+  int32_t *lo;     // [G + 1]
+  int rows_max;
+  static size_t bytes(int G) { return sizeof(int32_t) * (size_t)(2 * G + 2); }
+  __device__ __forceinline__ Table(void *mem, int G, int rows_max_)
+      : start(static_cast<int32_t *>(mem)), lo(start + G + 1), rows_max(rows_max_) {}
+  __device__ __forceinline__ int rows(int g) const { return max(0, lo[g + 1] - lo[g]); }
 };
 
 __device__ __forceinline__ void split_rows(int n, int rows_max, int &base, int &ntt) {
@@ -56,23 +53,24 @@ __device__ __forceinline__ void split_rows(int n, int rows_max, int &base, int &
 }
 
 // Every thread of the block calls; ends with the table complete for all.
-__device__ __forceinline__ void build_table(const Table &t, const int32_t *off, int G, int64_t rows,
-                                            int rows_max, int ft, int32_t *status) {
-  for (int g = threadIdx.x; g < G; g += blockDim.x) {
-    int lo, n, base, ntt;
-    group_bounds(off, g, rows, lo, n, status);
-    split_rows(n, rows_max, base, ntt);
-    t.lo[g] = lo;
-    t.n[g] = n;
-    t.base[g] = base;
-    t.start[g] = ntt * ft;
+__device__ __forceinline__ void build_table(const Table &t, const int32_t *__restrict__ off, int G,
+                                            int64_t rows, int ft, int32_t *status) {
+  for (int g = threadIdx.x; g <= G; g += blockDim.x) {
+    const int64_t a = off[g];
+    if (a < 0 || a > rows || (g < G && off[g + 1] < a)) set_status(status, MOE_ERR_RANGE);
+    t.lo[g] = (int)(a < 0 ? 0 : a > rows ? rows : a);
   }
   __syncthreads();
   if (threadIdx.x < 32) {  // exclusive prefix: a lane owns a run of groups
     const int lane = threadIdx.x, per = (G + 31) / 32;
     const int g0 = min(G, lane * per), g1 = min(G, g0 + per);
     int local = 0;
-    for (int g = g0; g < g1; ++g) local += t.start[g];
+    for (int g = g0; g < g1; ++g) {
+      int base, ntt;
+      split_rows(t.rows(g), t.rows_max, base, ntt);
+      t.start[g] = ntt * ft;
+      local += ntt * ft;
+    }
     int inc = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -106,8 +104,9 @@ __device__ __forceinline__ Tile find_tile(const Table &t, int tile, int G) {
   }
   Tile r;
   r.g = lo;
-  const int n = t.n[lo], base = t.base[lo];
-  r.ntt = (n + base - 1) / base;
+  const int n = t.rows(lo);
+  int base;
+  split_rows(n, t.rows_max, base, r.ntt);
   const int local = tile - t.start[lo];
   r.ft = local / r.ntt;
   r.tt = local - r.ft * r.ntt;

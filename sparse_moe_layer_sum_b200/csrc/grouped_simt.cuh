@@ -45,10 +45,10 @@ __global__ void __launch_bounds__(THREADS) product(Args p) {
   extern __shared__ float smem[];
   float(*As)[B + 4] = reinterpret_cast<float(*)[B + 4]>(smem);
   float(*Bs)[B + 4] = reinterpret_cast<float(*)[B + 4]>(smem + BK * (B + 4));
-  Table tab(smem + 2 * BK * (B + 4), p.G);
+  Table tab(smem + 2 * BK * (B + 4), p.G, B);
   const int cols = DIR == LIN ? p.n : p.k;  // columns of C
   const int ftiles = (cols + B - 1) / B, rtiles = (p.n + B - 1) / B;
-  build_table(tab, p.offsets, p.G, p.rows, B, ftiles, p.status);
+  build_table(tab, p.offsets, p.G, p.rows, ftiles, p.status);
   const int total = DIR == DW ? 0 : tab.start[p.G];
   const int64_t tiles = DIR == DW ? (int64_t)p.G * rtiles * ftiles : total;
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(THREADS) product(Args p) {
       nr = min(B, p.n - (int)r0);
       c0 = (local % ftiles) * B;
       k0 = tab.lo[g];
-      kc = tab.n[g];
+      kc = tab.rows(g);
       if (kc == 0 && p.accumulate) continue;
     } else {
       const Tile t = find_tile(tab, (int)tile, p.G);

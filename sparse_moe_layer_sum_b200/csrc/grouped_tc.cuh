@@ -214,7 +214,8 @@ struct RowCfg {
   static constexpr int NBUF = 2 * ACC <= 512 ? 2 : 1;
   static constexpr int COLS = NBUF * ACC;
   static constexpr uint32_t TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static constexpr int BAR = STAGES * STAGE;
+  static constexpr int XBUF = STAGES * STAGE;  // UP, BWD: 2 KB per epilogue warp
+  static constexpr int BAR = XBUF + (OP == UP || OP == BWD ? EPI * 2048 : 0);
   static constexpr int NBARS = 2 * STAGES + 5;
   static constexpr int MISC = BAR + NBARS * 8;
   static constexpr int TAB = (MISC + 16 + 4 * STAGES + 15) / 16 * 16;
@@ -224,24 +225,10 @@ struct RowCfg {
   static constexpr int STEP = 32 * (EPI / 4);   // between a warp's 32-row chunks
   static constexpr int NCH = BN / STEP;         // chunks of a warp and A tile
   static_assert(OP != UP || AT == 2, "UP pairs w1 and w3");
+  static_assert(OP != BWD || AT == 1, "BWD finishes one A tile");
+  static_assert((OP != UP && OP != BWD) || SEGS, "UP and BWD finish from registers");
   static_assert(!SEGS || (NBUF == 2 && AT * NCH <= 4), "sums in registers");
 };
-
-// The sum over the 32 lanes of each of 32 values; lane j returns value j's.
-__device__ __forceinline__ float lane_sums(float (&v)[32]) {
-  const int lane = threadIdx.x % 32;
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
-    const bool up = lane & w;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float send = up ? v[i] : v[i + w];
-      const float keep = up ? v[i + w] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
-    }
-  }
-  return v[0];
-}
 
 // The result of one accumulator chunk: lane l holds feature fw + l of the 32
 // rows from row0 on, the first nv of which belong to the tile.
@@ -259,81 +246,113 @@ __device__ __forceinline__ void finish_rows(const RowParams &p, const float (&v)
   }
 }
 
-// A warp holds the 32 features of one scale block: the block's largest
-// magnitude is one warp reduction per row and projection.
-__device__ __forceinline__ void finish_up(const RowParams &p, const float (&va)[32],
-                                          const float (&vu)[32], int fw, int row0, int nv) {
-  const int lane = threadIdx.x % 32, f = fw + lane;
+// UP and BWD finish a few rows of a chunk at a time from shared memory, where
+// a lane takes 4 consecutive features of one row and a warp 4 rows: whole
+// words of codes, 8-byte vectors of results, and one copy of the code in a
+// rolled loop (straight-line code for 128 sums per lane stalled on
+// instruction fetches).  x: [rows][32 features] of this warp.
+
+// 8 rows of a and u.  The 32 features are one scale block, so its largest
+// magnitude is a reduction over the 8 lanes of a row.
+__device__ __forceinline__ void finish_up(const RowParams &p, const float *x, int fw, int row0,
+                                          int nv) {
+  const int lane = threadIdx.x % 32, f = fw + lane % 8 * 4;
   const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
-  size_t at = (size_t)row0 * p.F + f;
-  int ea = 0, eu = 0;  // lane j keeps row j's scales
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const float a = va[j], u = vu[j];
-    const int ja = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(a)));
-    const int ju = ckpt::scale_byte(__reduce_max_sync(0xffffffffu, ckpt::finite_bits(u)));
-    if (lane == j) {
-      ea = ja;
-      eu = ju;
+  for (int s = 0; s < 2; ++s) {
+    const int r = s * 4 + lane / 8;
+    const float4 a4 = *reinterpret_cast<const float4 *>(x + r * 32 + lane % 8 * 4);
+    const float4 u4 = *reinterpret_cast<const float4 *>(x + 256 + r * 32 + lane % 8 * 4);
+    const float a[4] = {a4.x, a4.y, a4.z, a4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+    uint32_t ma = 0, mu = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ma = max(ma, ckpt::finite_bits(a[i]));
+      mu = max(mu, ckpt::finite_bits(u[i]));
     }
-    if (j < nv && f < p.F) {
-      static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(a * ckpt::sigmoid<bf16>(a) * u);
-      const uint16_t c = f32x2_to_e4m3x2(ckpt::scaled(a, ckpt::inv_scale_of(ja)),
-                                         ckpt::scaled(u, ckpt::inv_scale_of(ju)));
-      p.saved.ca[at] = (uint8_t)(c & 0xffu);
-      p.saved.cu[at] = (uint8_t)(c >> 8);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      mu = max(mu, __shfl_xor_sync(0xffffffffu, mu, o));
     }
-    at += p.F;
-  }
-  if (lane < nv && fw < p.F) {
-    const size_t sat = (size_t)(row0 + lane) * nb + fw / ckpt::BLOCK;
-    p.saved.ea[sat] = (uint8_t)ea;
-    p.saved.eu[sat] = (uint8_t)eu;
+    if (r >= nv || f >= p.F) continue;
+    const int ea = ckpt::scale_byte(ma), eu = ckpt::scale_byte(mu);
+    const float ia = ckpt::inv_scale_of(ea), iu = ckpt::inv_scale_of(eu);
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = a[i] * ckpt::sigmoid<bf16>(a[i]) * u[i];
+    const size_t at = (size_t)(row0 + r) * p.F + f;
+    *reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + at) = make_uint2(pack(h[0], h[1]), pack(h[2], h[3]));
+    *reinterpret_cast<uint32_t *>(p.saved.ca + at) =
+        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(a[0], ia), ckpt::scaled(a[1], ia)) |
+        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(a[2], ia), ckpt::scaled(a[3], ia)) << 16;
+    *reinterpret_cast<uint32_t *>(p.saved.cu + at) =
+        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(u[0], iu), ckpt::scaled(u[1], iu)) |
+        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(u[2], iu), ckpt::scaled(u[3], iu)) << 16;
+    if (lane % 8 == 0) {
+      const size_t sat = (size_t)(row0 + r) * nb + fw / ckpt::BLOCK;
+      p.saved.ea[sat] = (uint8_t)ea;
+      p.saved.eu[sat] = (uint8_t)eu;
+    }
   }
 }
 
-// dh in, the gradients out; the chunk's terms of dgate are summed over the
-// warp's 32 features and left in `part`.
-__device__ __forceinline__ void finish_bwd(const RowParams &p, float (&v)[32], int fw, int row0,
-                                           int nv) {
-  const int lane = threadIdx.x % 32, f = fw + lane;
-  const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
-  if (fw >= p.F) return;
-  // lane j: the scales and the gate of row j
-  const bool mine = lane < nv;
-  const size_t sat = (size_t)(row0 + lane) * nb + fw / ckpt::BLOCK;
-  const int ea = mine ? p.saved.ea[sat] : 0, eu = mine ? p.saved.eu[sat] : 0;
-  const float gt = mine && p.gate ? p.gate[row0 + lane] : 1.0f;
-  const size_t at0 = (size_t)row0 * p.F + f;
+// 16 rows of dh: what they need from memory, loaded ahead of the sums.
+struct BwdRows {
+  uint32_t ca[4], cu[4];
+  int e[4];
+  float g[4];
+  __device__ __forceinline__ void load(const RowParams &p, int fw, int row0, int nv) {
+    const int lane = threadIdx.x % 32, f = fw + lane % 8 * 4;
+    const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
 #pragma unroll
-  for (int j0 = 0; j0 < 32; j0 += 16) {
-    uint16_t q[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const bool on = j0 + j < nv && f < p.F;
-      const size_t at = at0 + (size_t)(j0 + j) * p.F;
-      q[j] = on ? (uint16_t)(__ldg(p.saved.ca + at) | __ldg(p.saved.cu + at) << 8) : 0;
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int r = j0 + j;
-      const float2 d = ckpt::decode2(q[j]);
-      const float a = d.x * ckpt::scale_of(__shfl_sync(0xffffffffu, ea, r));
-      const float u = d.y * ckpt::scale_of(__shfl_sync(0xffffffffu, eu, r));
-      const float g = __shfl_sync(0xffffffffu, gt, r);
-      float xa, xu, xh;
-      const float s = ckpt::swiglu_grad<bf16>(a, u, v[r], g, xa, xu, xh);
-      v[r] = f < p.F ? s : 0.0f;
+    for (int s = 0; s < 4; ++s) {
+      const int r = s * 4 + lane / 8;
+      ca[s] = cu[s] = 0u;
+      e[s] = 0;
+      g[s] = 1.0f;
       if (r < nv && f < p.F) {
-        const size_t at = at0 + (size_t)r * p.F;
-        p.da[at] = __float2bfloat16_rn(xa);
-        p.du[at] = __float2bfloat16_rn(xu);
-        p.hg[at] = __float2bfloat16_rn(xh);
+        const size_t at = (size_t)(row0 + r) * p.F + f, sat = (size_t)(row0 + r) * nb + fw / ckpt::BLOCK;
+        ca[s] = __ldg(reinterpret_cast<const uint32_t *>(p.saved.ca + at));
+        cu[s] = __ldg(reinterpret_cast<const uint32_t *>(p.saved.cu + at));
+        e[s] = __ldg(p.saved.ea + sat) | __ldg(p.saved.eu + sat) << 8;
+        if (p.gate) g[s] = __ldg(p.gate + row0 + r);
       }
     }
   }
-  const float sum = lane_sums(v);
-  if (mine) p.part[(size_t)(fw / ckpt::BLOCK) * p.rows + row0 + lane] = sum;
+};
+
+__device__ __forceinline__ void finish_bwd(const RowParams &p, const BwdRows &in, const float *x, int fw,
+                                           int row0, int nv) {
+  const int lane = threadIdx.x % 32, f = fw + lane % 8 * 4;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int r = s * 4 + lane / 8;
+    const float4 d4 = *reinterpret_cast<const float4 *>(x + r * 32 + lane % 8 * 4);
+    const float dh[4] = {d4.x, d4.y, d4.z, d4.w};
+    const float sa = ckpt::scale_of(in.e[s] & 0xff), su = ckpt::scale_of(in.e[s] >> 8);
+    float da[4], du[4], hg[4], term = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float2 a = ckpt::decode2((uint16_t)(in.ca[s] >> (8 * i))), u = ckpt::decode2((uint16_t)(in.cu[s] >> (8 * i)));
+      term += ckpt::swiglu_grad<bf16>(a.x * sa, u.x * su, dh[i], in.g[s], da[i], du[i], hg[i]);
+      term += ckpt::swiglu_grad<bf16>(a.y * sa, u.y * su, dh[i + 1], in.g[s], da[i + 1], du[i + 1], hg[i + 1]);
+    }
+    const bool on = r < nv && f < p.F;
+    if (!on) term = 0.0f;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+    if (!on) continue;
+    const size_t at = (size_t)(row0 + r) * p.F + f;
+    *reinterpret_cast<uint2 *>(p.da + at) = make_uint2(pack(da[0], da[1]), pack(da[2], da[3]));
+    *reinterpret_cast<uint2 *>(p.du + at) = make_uint2(pack(du[0], du[1]), pack(du[2], du[3]));
+    *reinterpret_cast<uint2 *>(p.hg + at) = make_uint2(pack(hg[0], hg[1]), pack(hg[2], hg[3]));
+    if (lane % 8 == 0) p.part[(size_t)(fw / ckpt::BLOCK) * p.rows + row0 + r] = term;
+  }
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *q) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
 }
 
 template <int OP, int CG, int AT, int BN, int STAGES, bool SEGS, typename TO>
@@ -349,7 +368,7 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 4);
   volatile int *pending = reinterpret_cast<volatile int *>(sm + C::MISC + 16);
-  const Table tab(sm + C::TAB, p.G);
+  const Table tab(sm + C::TAB, p.G, BN);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -382,7 +401,7 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
       tmem_relinquish();
     }
   }
-  build_table(tab, p.offsets, p.G, p.rows, BN, (p.F + C::FEAT - 1) / C::FEAT, p.status);
+  build_table(tab, p.offsets, p.G, p.rows, (p.F + C::FEAT - 1) / C::FEAT, p.status);
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();  // the pair's barriers exist before any remote arrive
@@ -531,9 +550,21 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
       if (SEGS) {
         // sum[a * NCH + ch]: chunk ch of A tile a
         float sum[AT * NCH][32];
+#pragma unroll
+        for (int i = 0; i < AT * NCH; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
         bool ok = true;
         for (int kb = 0; kb < p.kb; kb += SEG) {
           if (!(ok = acquire())) break;
+          if (OP == BWD && kb == 0 && fw < p.F) {
+            // the codes are needed after the last segment: into L2 by then
+            for (int c = half * 32 + lane; c < t.nvalid; c += STEP) {
+              const size_t at = (size_t)(t.row0 + c) * p.F + fw;
+              prefetch_l2(p.saved.ca + at);
+              prefetch_l2(p.saved.cu + at);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < AT * NCH; ++i) {
             const int c0 = half * 32 + i % NCH * STEP;
@@ -542,22 +573,44 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
             tmem_ld_32x32b_x32(tb + (uint32_t)(i / NCH * BN + c0), v);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              sum[i][j] = kb == 0 ? __uint_as_float(v[j]) : sum[i][j] + __uint_as_float(v[j]);
+            for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(v[j]);
           }
           release();
         }
         if (!ok) break;
+        if constexpr (OP == UP || OP == BWD) {
+          // HR rows at a time: the registers of part `h` go through x
+          constexpr int HR = OP == UP ? 8 : 16, PARTS = 32 / HR;
+          float *x = reinterpret_cast<float *>(sm + C::XBUF) + (warp - 4) * 512;
+#pragma unroll 1
+          for (int h = 0; h < NCH * PARTS; ++h) {
+            const int c0 = half * 32 + h / PARTS * STEP + h % PARTS * HR;
+            if (c0 >= t.nvalid) continue;
+            BwdRows in;
+            if (OP == BWD) in.load(p, fw, t.row0 + c0, t.nvalid - c0);
+            __syncwarp();  // x has been read
 #pragma unroll
-        for (int i = 0; i < (OP == UP ? 1 : AT) * NCH; ++i) {
-          const int c0 = half * 32 + i % NCH * STEP, fa = fw + i / NCH * BM * CG;
-          if (c0 >= t.nvalid) continue;
-          if (OP == UP)
-            finish_up(p, sum[i], sum[(AT - 1) * NCH + i], fa, t.row0 + c0, t.nvalid - c0);
-          else if (OP == BWD)
-            finish_bwd(p, sum[i], fa, t.row0 + c0, t.nvalid - c0);
-          else
-            finish_rows<TO>(p, sum[i], fa, t.row0 + c0, t.nvalid - c0);
+            for (int k = 0; k < NCH * PARTS; ++k)
+              if (k == h) {
+#pragma unroll
+                for (int r = 0; r < HR; ++r) {
+                  x[r * 32 + lane] = sum[k / PARTS][k % PARTS * HR + r];
+                  if (OP == UP) x[256 + r * 32 + lane] = sum[(AT - 1) * NCH + k / PARTS][k % PARTS * HR + r];
+                }
+              }
+            __syncwarp();
+            if (OP == UP)
+              finish_up(p, x, fw, t.row0 + c0, t.nvalid - c0);
+            else
+              finish_bwd(p, in, x, fw, t.row0 + c0, t.nvalid - c0);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < AT * NCH; ++i) {
+            const int c0 = half * 32 + i % NCH * STEP;
+            if (c0 < t.nvalid)
+              finish_rows<TO>(p, sum[i], fw + i / NCH * BM * CG, t.row0 + c0, t.nvalid - c0);
+          }
         }
       } else {
         // chunks are read in batches; the accumulator goes back right after

@@ -438,7 +438,9 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
   if (!ws || ws_bytes < moe_swiglu_checkpoint_workspace_size(s, dt)) return MOE_ERR_WORKSPACE;
   cudaStream_t cs = as_stream(stream);
   const ckpt::Saved sv{codes_a, exps_a, codes_u, exps_u};
-  if (dt == MOE_BF16 && tc_operand(x, s->k, dt) && tc_operand(w1, s->k, dt) && tc_operand(w3, s->k, dt)) {
+  // the tensor-core kernel writes 4 hidden features of a row at a time
+  if (dt == MOE_BF16 && tc_operand(x, s->k, dt) && tc_operand(w1, s->k, dt) && tc_operand(w3, s->k, dt) &&
+      s->n % 4 == 0 && aligned(h, 8) && aligned(codes_a, 4) && aligned(codes_u, 4)) {
     tcg::RowParams r = {};
     r.offsets = offsets;
     r.out = h;
@@ -485,7 +487,8 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
   cudaStream_t cs = as_stream(stream);
   const ckpt::Saved sv{const_cast<uint8_t *>(codes_a), const_cast<uint8_t *>(exps_a),
                        const_cast<uint8_t *>(codes_u), const_cast<uint8_t *>(exps_u)};
-  if (dt == MOE_BF16 && tc_operand(dy, s->k, dt) && tc_operand(w2, s->n, dt)) {
+  if (dt == MOE_BF16 && tc_operand(dy, s->k, dt) && tc_operand(w2, s->n, dt) && aligned(codes_a, 4) &&
+      aligned(codes_u, 4) && aligned(da, 8) && aligned(du, 8) && aligned(hg, 8)) {
     tcg::RowParams r = {};
     r.offsets = offsets;
     r.status = dev_status;
