@@ -102,9 +102,12 @@ moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps, int64_t r
  * straight from their fp32 sums (s->n is the hidden width, s->k the model's).
  *   x [rows, k], w1, w3 [groups, n, k] of type dt; h [rows, n] of type dt
  *   codes_a, codes_u [rows, n], exps_a, exps_u [rows, ceil(n / 32)] uint8
- *   ws  moe_swiglu_checkpoint_workspace_size bytes (may be 0: ws may be NULL)
+ *   ws  moe_swiglu_checkpoint_workspace_size bytes (0: ws may be NULL).
+ *       aligned: 1 when x, w1, w3, h and the codes are all 16-byte aligned,
+ *       as fresh allocations are; 0 asks for enough for any operands.
  */
-size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt);
+size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                            int32_t aligned);
 moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const void *x, moe_dtype dt,
                                  const void *w1, const void *w3, const int32_t *offsets, void *h,
                                  uint8_t *codes_a, uint8_t *exps_a, uint8_t *codes_u,
@@ -122,9 +125,11 @@ moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const void *x, moe_
  * hg is the operand of w2's gradient, grouped_linear_dw(dy, hg).
  *   dy [rows, k], w2 [groups, k, n] of type dt (s->n the hidden width)
  *   gate [rows] fp32 or NULL (1); da, du, hg [rows, n]; dgate [rows] fp32
- *   ws  moe_swiglu_backward_workspace_size bytes
+ *   ws  moe_swiglu_backward_workspace_size bytes; aligned as above, for dy,
+ *       w2, the codes, da, du and hg
  */
-size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt);
+size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                          int32_t aligned);
 moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
                                const void *w2, const uint8_t *codes_a, const uint8_t *exps_a,
                                const uint8_t *codes_u, const uint8_t *exps_u, const float *gate,

@@ -104,10 +104,10 @@ SIGNATURES = {
     ("moe_train", "moe_checkpoint_rows"): (_i32, [_vp, _i32, _i64, _i32, _vp, _vp, _vp]),
     ("moe_train", "moe_restore_rows"): (
         _i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _vp, _vp]),
-    ("moe_train", "moe_swiglu_checkpoint_workspace_size"): (_sz, [_gsp, _i32]),
+    ("moe_train", "moe_swiglu_checkpoint_workspace_size"): (_sz, [_gsp, _i32, _i32]),
     ("moe_train", "moe_swiglu_checkpoint"): (
         _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
-    ("moe_train", "moe_swiglu_backward_workspace_size"): (_sz, [_gsp, _i32]),
+    ("moe_train", "moe_swiglu_backward_workspace_size"): (_sz, [_gsp, _i32, _i32]),
     ("moe_train", "moe_swiglu_backward"): (
         _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                _vp, _vp]),

@@ -32,10 +32,14 @@ moe_status check_shape(const moe_grouped_shape *s) {
   return MOE_OK;
 }
 
+// SMs of the current device, asked once per device; 0 if that fails.
 int sm_count() {
+  static int known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && known[dev]) return known[dev];
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev] = n;
   return n;
 }
 
@@ -137,12 +141,13 @@ bool tensor_map(CUtensorMap *m, const void *base, moe_dtype dt, uint64_t planes,
 }
 
 // One block, or one pair of blocks, per SM or SM pair.
-template <typename... A>
-moe_status launch_persistent(void (*kern)(A...), int threads, size_t smem, int cg, int64_t tiles,
+template <auto kern, typename... A>
+moe_status launch_persistent(int threads, size_t smem, int cg, int64_t tiles,
                              cudaStream_t s, A... args) {
-  if (smem > 232448) return MOE_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  constexpr size_t SMEM_MAX = 232448;
+  if (smem > SMEM_MAX) return MOE_ERR_UNSUPPORTED;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const int nsm = sm_count();
   if (nsm < 2) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -159,22 +164,25 @@ moe_status launch_persistent(void (*kern)(A...), int threads, size_t smem, int c
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  if (cg == 2) {
-    // SM pairs that can be resident together, looked up once per kernel and device
-    static int resident[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    int n = dev < 64 ? resident[dev] : 0;
-    if (n == 0) {
+  // asked once per kernel and device: the shared-memory limit, and how many
+  // SM pairs can be resident together
+  static int ready[64];
+  int n = dev < 64 ? ready[dev] : 0;
+  if (n == 0) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+    n = (int)units;
+    if (cg == 2) {
       cfg.gridDim = dim3((unsigned)(units * 2));
       if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();  // not sticky: the launch below decides
         n = (int)units;
       }
-      if (dev < 64) resident[dev] = n;
     }
-    if (n < units) units = n;
+    if (dev < 64) ready[dev] = n;
   }
+  if (n < units) units = n;
   if (tiles < units) units = tiles > 0 ? tiles : 1;
   cfg.gridDim = dim3((unsigned)(units * cg));
   if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return MOE_ERR_CUDA;
@@ -220,7 +228,7 @@ moe_status launch_rows(const moe_grouped_shape *s, const void *w0, const void *w
   p.kb0 = (contract + tcg::BK - 1) / tcg::BK;
   p.kb = x1 ? 2 * p.kb0 : p.kb0;
   const int64_t tiles = row_tiles(s, BN) * ((F + C::FEAT - 1) / C::FEAT);
-  return launch_persistent(tcg::rows_gemm<OP, CG, AT, BN, STAGES, SEGS, TO>, C::NT, C::smem(p.G), CG, tiles,
+  return launch_persistent<tcg::rows_gemm<OP, CG, AT, BN, STAGES, SEGS, TO>>(C::NT, C::smem(p.G), CG, tiles,
                            st, m.a0, m.a1, m.b0, m.b1, (const tcg::RowParams)p);
 }
 
@@ -243,6 +251,17 @@ moe_status tc_rows(const Product &p, int F, int contract) {
     if (F < 512) return run(launch_rows<OP, 1, 1, 256, 4, false, TO>);
     return run(launch_rows<OP, 2, 2, 256, 4, false, TO>);
   }
+}
+
+int scale_blocks(int n) { return (n + ckpt::BLOCK - 1) / ckpt::BLOCK; }
+
+// Sizes the tensor-core kernels take: rows of 16 bytes, and 4 hidden features
+// written at a time.
+bool tc_up_sizes(const moe_grouped_shape *s, moe_dtype dt) {
+  return dt == MOE_BF16 && s->k % 8 == 0 && s->n % 4 == 0;
+}
+bool tc_bwd_sizes(const moe_grouped_shape *s, moe_dtype dt) {
+  return dt == MOE_BF16 && s->k % 8 == 0 && s->n % 8 == 0;
 }
 
 // The first matmul with its checkpoint (n hidden features from k), and the
@@ -272,7 +291,7 @@ moe_status launch_dw(const Product &p) {
     return MOE_ERR_CUDA;
   const tcg::DwParams d{p.offsets, s->groups, s->n, s->k, s->rows, p.out, p.accumulate, p.status};
   const int64_t tiles = (int64_t)s->groups * ((s->n + C::FEAT - 1) / C::FEAT) * ((s->k + 255) / 256);
-  return launch_persistent(tcg::dw_gemm<TO, AT>, C::NT, (size_t)C::BYTES, 2, tiles, p.stream, a, b, c, d);
+  return launch_persistent<tcg::dw_gemm<TO, AT>>(C::NT, (size_t)C::BYTES, 2, tiles, p.stream, a, b, c, d);
 }
 
 moe_status tc_dw(const Product &p) {
@@ -370,7 +389,7 @@ MOE_EXPORT moe_status moe_checkpoint_rows(const void *src, moe_dtype dt, int64_t
   if (rows == 0) return MOE_OK;
   if (!src || !codes || !exps) return MOE_ERR_INVALID;
   cudaStream_t cs = as_stream(stream);
-  const int nb = (k + ckpt::BLOCK - 1) / ckpt::BLOCK;
+  const int nb = scale_blocks(k);
   if (k % 8 == 0 && aligned(src, 16) && aligned(codes, 8)) {
     const int per = 32 * ckpt::UNROLL;
     const unsigned grid = row_grid(rows * ((nb * 4 + per - 1) / per));
@@ -399,7 +418,7 @@ MOE_EXPORT moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps
   if (n == 0) return MOE_OK;
   if (!out || (rows > 0 && (!codes || !exps))) return MOE_ERR_INVALID;
   cudaStream_t cs = as_stream(stream);
-  const int nb = (k + ckpt::BLOCK - 1) / ckpt::BLOCK;
+  const int nb = scale_blocks(k);
   if (k % 8 == 0 && aligned(out, 16) && aligned(codes, 8)) {
     const int per = 32 * ckpt::UNROLL;
     const unsigned grid = row_grid(n * ((nb * 4 + per - 1) / per));
@@ -417,10 +436,11 @@ MOE_EXPORT moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps
   return launch_status();
 }
 
-MOE_EXPORT size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt) {
+MOE_EXPORT size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                                       int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
-  // the two projections in fp32, for the CUDA cores
-  return 2 * align_up((size_t)s->rows * s->n * 4, 256);
+  if (aligned && tc_up_sizes(s, dt)) return 0;
+  return 2 * align_up((size_t)s->rows * s->n * 4, 256);  // the two projections in fp32
 }
 
 MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const void *x,
@@ -435,12 +455,13 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
   if (s->rows == 0) return MOE_OK;
   if (!x || !w1 || !w3 || !offsets || !h || !codes_a || !exps_a || !codes_u || !exps_u)
     return MOE_ERR_INVALID;
-  if (!ws || ws_bytes < moe_swiglu_checkpoint_workspace_size(s, dt)) return MOE_ERR_WORKSPACE;
   cudaStream_t cs = as_stream(stream);
   const ckpt::Saved sv{codes_a, exps_a, codes_u, exps_u};
-  // the tensor-core kernel writes 4 hidden features of a row at a time
-  if (dt == MOE_BF16 && tc_operand(x, s->k, dt) && tc_operand(w1, s->k, dt) && tc_operand(w3, s->k, dt) &&
-      s->n % 4 == 0 && aligned(h, 8) && aligned(codes_a, 4) && aligned(codes_u, 4)) {
+  const bool tc = tc_up_sizes(s, dt) && aligned(x, 16) && aligned(w1, 16) && aligned(w3, 16) &&
+                  aligned(h, 8) && aligned(codes_a, 4) && aligned(codes_u, 4);
+  const size_t need = moe_swiglu_checkpoint_workspace_size(s, dt, tc);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (tc) {
     tcg::RowParams r = {};
     r.offsets = offsets;
     r.out = h;
@@ -454,7 +475,7 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
     return st;
   if ((st = run_linear({s, dt, MOE_F32, x, w3, nullptr, nullptr, offsets, u, 0, dev_status, cs})) != MOE_OK)
     return st;
-  const unsigned grid = row_grid(s->rows * ((s->n + ckpt::BLOCK - 1) / ckpt::BLOCK));
+  const unsigned grid = row_grid(s->rows * scale_blocks(s->n));
   if (dt == MOE_F32)
     ckpt::swiglu_save<<<grid, ckpt::ROW_THREADS, 0, cs>>>(a, u, offsets, s->groups, s->rows, s->n, static_cast<float *>(h), sv);
   else
@@ -462,11 +483,12 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
   return launch_status();
 }
 
-MOE_EXPORT size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt) {
+MOE_EXPORT size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                                     int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
-  // dh in fp32 for the CUDA cores; the tensor-core path keeps one term of
-  // dgate for 32 of its values
-  return align_up((size_t)s->rows * s->n * 4, 256);
+  // one term of dgate for 32 hidden features, or dh in fp32
+  if (aligned && tc_bwd_sizes(s, dt)) return (size_t)s->rows * scale_blocks(s->n) * 4;
+  return (size_t)s->rows * s->n * 4;
 }
 
 MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
@@ -483,12 +505,13 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
   if (!dy || !w2 || !codes_a || !exps_a || !codes_u || !exps_u || !offsets || !da || !du || !hg ||
       !dgate)
     return MOE_ERR_INVALID;
-  if (!ws || ws_bytes < moe_swiglu_backward_workspace_size(s, dt)) return MOE_ERR_WORKSPACE;
   cudaStream_t cs = as_stream(stream);
   const ckpt::Saved sv{const_cast<uint8_t *>(codes_a), const_cast<uint8_t *>(exps_a),
                        const_cast<uint8_t *>(codes_u), const_cast<uint8_t *>(exps_u)};
-  if (dt == MOE_BF16 && tc_operand(dy, s->k, dt) && tc_operand(w2, s->n, dt) && aligned(codes_a, 4) &&
-      aligned(codes_u, 4) && aligned(da, 8) && aligned(du, 8) && aligned(hg, 8)) {
+  const bool tc = tc_bwd_sizes(s, dt) && aligned(dy, 16) && aligned(w2, 16) && aligned(codes_a, 4) &&
+                  aligned(codes_u, 4) && aligned(da, 8) && aligned(du, 8) && aligned(hg, 8);
+  if (!ws || ws_bytes < moe_swiglu_backward_workspace_size(s, dt, tc)) return MOE_ERR_WORKSPACE;
+  if (tc) {
     tcg::RowParams r = {};
     r.offsets = offsets;
     r.status = dev_status;
@@ -500,7 +523,7 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
     r.part = static_cast<float *>(ws);
     if ((st = tc_bwd(s, dy, w2, r, cs)) != MOE_OK) return st;
     tcg::sum_parts<<<(unsigned)((s->rows + 255) / 256), 256, 0, cs>>>(
-        r.part, offsets, s->groups, s->rows, (s->n + ckpt::BLOCK - 1) / ckpt::BLOCK, dgate);
+        r.part, offsets, s->groups, s->rows, scale_blocks(s->n), dgate);
     return launch_status();
   }
   float *dh = static_cast<float *>(ws);

@@ -57,15 +57,29 @@ def _check(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device
     return dev
 
 
+_fn: dict = {}  # entry points of moe_train, looked up once
+
+
+def _entry(sym: str):
+    f = _fn.get(sym)
+    if f is None:
+        f = _fn[sym] = fn("moe_train", sym)
+    return f
+
+
 def _call(dev: torch.device, sym: str, *args) -> None:
-    """Call `sym` of moe_train with `dev` current, on its current stream."""
-    f = fn("moe_train", sym)
-    if dev.index == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream().cuda_stream)
+    """Call `sym` of moe_train with `dev` current, on its current stream.  (The
+    raw stream handle is read directly: torch.cuda.current_stream() alone takes
+    as long as the rest of a call.)"""
+    f = _entry(sym)
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream().cuda_stream)
-    check(st, sym)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st:
+        check(st, sym)
 
 
 def _groups(offsets: torch.Tensor) -> int:
@@ -201,8 +215,10 @@ def restore_rows(ckpt: Checkpoint, index: Optional[torch.Tensor] = None, *,
     return out
 
 
-def _workspace(sym: str, shape: MoEGroupedShape, dt: int, dev):
-    need = fn("moe_train", sym)(ctypes.byref(shape), dt)
+def _workspace(sym: str, shape: MoEGroupedShape, dt: int, dev, *operands: torch.Tensor):
+    """Device workspace of a swiglu call (None if it needs none)."""
+    aligned = not any(t.data_ptr() % 16 for t in operands)
+    need = _entry(sym)(ctypes.byref(shape), dt, int(aligned))
     return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
 
 
@@ -220,7 +236,8 @@ def swiglu_checkpoint(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, offse
     h = torch.empty(rows, n, dtype=x.dtype, device=dev)
     a, u = _empty_ckpt(rows, n, dev), _empty_ckpt(rows, n, dev)
     shape = MoEGroupedShape(G, n, x.shape[1], rows)
-    ws = _workspace("moe_swiglu_checkpoint_workspace_size", shape, dt, dev)
+    ws = _workspace("moe_swiglu_checkpoint_workspace_size", shape, dt, dev, x, w1, w3, h, a.codes,
+                    u.codes)
     _call(dev, "moe_swiglu_checkpoint", ctypes.byref(shape), x.data_ptr(), dt, w1.data_ptr(),
           w3.data_ptr(), offsets.data_ptr(), h.data_ptr(), a.codes.data_ptr(), a.exps.data_ptr(),
           u.codes.data_ptr(), u.exps.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
@@ -247,7 +264,8 @@ def swiglu_backward(dy: torch.Tensor, w2: torch.Tensor, a: Checkpoint, u: Checkp
     da, du, hg = (torch.empty(rows, n, dtype=dy.dtype, device=dev) for _ in range(3))
     dgate = torch.empty(rows, dtype=torch.float32, device=dev)
     shape = MoEGroupedShape(G, n, k, rows)
-    ws = _workspace("moe_swiglu_backward_workspace_size", shape, dt, dev)
+    ws = _workspace("moe_swiglu_backward_workspace_size", shape, dt, dev, dy, w2, a.codes, u.codes,
+                    da, du, hg)
     _call(dev, "moe_swiglu_backward", ctypes.byref(shape), dy.data_ptr(), dt, w2.data_ptr(),
           a.codes.data_ptr(), a.exps.data_ptr(), u.codes.data_ptr(), u.exps.data_ptr(), _ptr(gate),
           offsets.data_ptr(), da.data_ptr(), du.data_ptr(), hg.data_ptr(), dgate.data_ptr(),
