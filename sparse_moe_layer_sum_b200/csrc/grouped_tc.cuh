@@ -841,44 +841,67 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------ MMA issuer (leader), tail rows (both SMs)
-    Ring r, acc;
-    bool ok = true;
-    for (int64_t tile = unit; ok && tile < total; tile += nunits) {
-      const Job j = job(tile);
-      if (j.kb == 0) continue;
-      const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
-      uint32_t d = 0;
-      for (int i = 0; i < j.kb; ++i) {
-        uint8_t *st = sm + r.stage * C::STAGE;
-        const bool first = i == 0 || (C::SEGS && i % SEG == 0);
-        if (leader && first) {
-          if (i > 0) {
-            if (lane == 0) commit<2>(accf + acc.stage);
-            acc.next(C::NBUF);
+    if (lane == 0 && leader) {
+      // -------------------------------------------------------- MMA issuer
+      Ring r, acc;
+      bool ok = true;
+      for (int64_t tile = unit; ok && tile < total; tile += nunits) {
+        const Job j = job(tile);
+        if (j.kb == 0) continue;
+        const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
+        uint32_t d = 0;
+        for (int i = 0; i < j.kb; ++i) {
+          const bool first = i == 0 || (C::SEGS && i % SEG == 0);
+          if (first) {
+            if (i > 0) {
+              commit<2>(accf + acc.stage);
+              acc.next(C::NBUF);
+            }
+            if (!(ok = wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status))) break;
+            d = tmem + (uint32_t)(acc.stage * AT * 256);
           }
-          if (!wait_warp(acce + acc.stage, acc.phase ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+          if (!(ok = wait_bounded(full + r.stage, r.phase, abort_flag, WAIT_NS, p.status))) break;
+          pending[r.stage] = -1;
           tc_fence_after();
-          d = tmem + (uint32_t)(acc.stage * AT * 256);
+          const uint32_t a = smem_u32(sm + r.stage * C::STAGE), b = a + AT * TILE;
+          const int steps = i == j.kb - 1 ? (j.tail + 15) / 16 : BK / 16;
+          for (int s = 0; s < steps; ++s)
+#pragma unroll
+            for (int c = 0; c < AT; ++c)
+              mma<2>(d + c * 256, desc_mn(a + c * TILE + s * 2048), desc_mn(b + s * 2048), idesc,
+                     first && s == 0 ? 0u : 1u);
+          commit<2>(empty + r.stage);
+          r.next(STAGES);
         }
-        const bool fix = j.fix(i);
-        // the SM that issues no MMAs follows the ring on its `tail` barriers
-        if ((fix || !leader) && !wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
-          ok = false;
+        if (!ok) break;
+        commit<2>(accf + acc.stage);
+        acc.next(C::NBUF);
+      }
+      if (!ok) {
+        mma_commit_pair(drained);
+        drain(drained, 0);
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------- tail rows, ahead of the MMAs
+    // (done by the issuing warp itself, this held up every tile of a short
+    // group: 455 -> 385 us for 32 groups of about 128 rows)
+    Ring r;
+    for (int64_t tile = unit; tile < total; tile += nunits) {
+      const Job j = job(tile);
+      for (int i = 0; i < j.kb; ++i) {
+        if (!wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
+          tile = total;
           break;
         }
-        if (fix) {
+        if (j.fix(i)) {
           // rows tail .. next multiple of 16 of every 64-column box: 128
           // bytes each, whole rows, so the swizzle does not matter
-          const int nz = 16 - j.tail % 16, nbox = 2 * AT + (j.nmma / 2 + 63) / 64;
-          for (int z = lane; z < nbox * nz * 8; z += 32) {
-            const int bx = z / (nz * 8), w = z % (nz * 8);
-            *reinterpret_cast<uint4 *>(st + bx * BOX + (j.tail + w / 8) * 128 + w % 8 * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
+          uint8_t *st = sm + r.stage * C::STAGE + j.tail * 128;
+          const int bytes = (16 - j.tail % 16) * 128, nbox = 2 * AT + (j.nmma / 2 + 63) / 64;
+          for (int bx = 0; bx < nbox; ++bx)
+            for (int at = lane * 16; at < bytes; at += 512)
+              *reinterpret_cast<uint4 *>(st + bx * BOX + at) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -886,37 +909,9 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
             arrive_cluster(mapa_shared(smem_u32(full + r.stage), 0));
           }
         }
-        if (leader) {
-          if (!wait_warp(full + r.stage, r.phase, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            pending[r.stage] = -1;
-            const uint32_t a = smem_u32(st), b = a + AT * TILE;
-            const int steps = i == j.kb - 1 ? (j.tail + 15) / 16 : BK / 16;
-            for (int s = 0; s < steps; ++s)
-#pragma unroll
-              for (int c = 0; c < AT; ++c)
-                mma<2>(d + c * 256, desc_mn(a + c * TILE + s * 2048), desc_mn(b + s * 2048), idesc,
-                       first && s == 0 ? 0u : 1u);
-            commit<2>(empty + r.stage);
-          }
-          __syncwarp();
-        }
         r.next(STAGES);
       }
-      if (!ok) break;
-      if (leader && lane == 0) commit<2>(accf + acc.stage);
-      __syncwarp();
-      acc.next(C::NBUF);
     }
-    if (!ok && leader && lane == 0) {
-      mma_commit_pair(drained);
-      drain(drained, 0);
-    }
-    __syncwarp();
   }
   } else {
     regs_high();

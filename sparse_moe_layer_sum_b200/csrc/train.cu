@@ -45,11 +45,11 @@ int sm_count() {
 
 // ------------------------------------------------------------ CUDA-core path
 
-template <typename TI, typename TO, int DIR, int B>
+template <typename TI, typename TO, int DIR, int T>
 moe_status launch_simt(const simt::Args &a, int64_t tiles, int nsm, cudaStream_t s) {
-  const size_t smem = simt::smem_bytes<B>(a.G);
-  const int64_t grid = tiles < (int64_t)nsm * 4 ? tiles : (int64_t)nsm * 4;
-  simt::product<TI, TO, DIR, B><<<(unsigned)grid, simt::THREADS, smem, s>>>(a);
+  const int64_t most = (int64_t)nsm * simt::Cfg<T>::BLOCKS;
+  const int64_t grid = tiles < most ? tiles : most;
+  simt::product<TI, TO, DIR, T><<<(unsigned)grid, simt::THREADS, simt::Cfg<T>::smem(a.G), s>>>(a);
   return launch_status();
 }
 
@@ -58,14 +58,15 @@ moe_status simt_tiles(const simt::Args &a, cudaStream_t s) {
   const int nsm = sm_count();
   if (nsm < 1) return MOE_ERR_CUDA;
   const int cols = DIR == simt::LIN ? a.n : a.k;
-  auto tiles = [&](int b) {
-    const int64_t ct = (cols + b - 1) / b;
-    return DIR == simt::DW ? (int64_t)a.G * ((a.n + b - 1) / b) * ct : (a.rows / b + a.G) * ct;
+  auto tiles = [&](int t) {
+    const int64_t ct = (cols + t - 1) / t;
+    return DIR == simt::DW ? (int64_t)a.G * ((a.n + t - 1) / t) * ct : (a.rows / t + a.G) * ct;
   };
-  // 128 x 128 tiles reuse each operand value twice as often as 64 x 64 ones;
-  // the smaller tiles where the larger would leave SMs without work
-  if (tiles(128) >= 2 * nsm) return launch_simt<TI, TO, DIR, 128>(a, tiles(128), nsm, s);
-  return launch_simt<TI, TO, DIR, 64>(a, tiles(64), nsm, s);
+  // the larger tile reuses each operand value more often; the smaller ones
+  // where the larger would leave SMs without work
+  if (tiles(128) >= 4 * nsm) return launch_simt<TI, TO, DIR, 128>(a, tiles(128), nsm, s);
+  if (tiles(64) >= nsm) return launch_simt<TI, TO, DIR, 64>(a, tiles(64), nsm, s);
+  return launch_simt<TI, TO, DIR, 32>(a, tiles(32), nsm, s);
 }
 
 template <int DIR>
