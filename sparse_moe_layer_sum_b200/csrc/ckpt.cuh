@@ -98,7 +98,7 @@ struct Vec8<bf16> {
       const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
   }
 };
 template <>
@@ -115,6 +115,13 @@ struct Vec8<float> {
   }
 };
 
+// un / per for the warps' work items; nearly always within 32 bits, where the
+// division costs a quarter.
+__device__ __forceinline__ int64_t item_row(int64_t un, int per) {
+  if (un <= 0xffffffffll) return (int64_t)((uint32_t)un / (uint32_t)per);
+  return un / per;
+}
+
 constexpr int ROW_THREADS = 256;
 constexpr int UNROLL = 4;  // eight-value chunks in flight per lane
 
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(ROW_THREADS) save_rows_v8(const TI *__restrict
   const int64_t units = rows * segs, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
        un += step) {
-    const int64_t row = un / segs;
+    const int64_t row = item_row(un, segs);
     const int c0 = (int)(un - row * segs) * 32 * UNROLL + lane;
     float v[UNROLL][8];
 #pragma unroll
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(ROW_THREADS) save_rows(const TI *__restrict__ 
   const int64_t units = rows * nb, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
        un += step) {
-    const int64_t row = un / nb;
+    const int64_t row = item_row(un, nb);
     const int b = (int)(un - row * nb), i = b * BLOCK + lane;
     const float v = i < k ? to_f(src[row * k + i]) : 0.0f;
     const int e = scale_byte(__reduce_max_sync(0xffffffffu, finite_bits(v)));
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(ROW_THREADS) load_rows_v8(const uint8_t *__res
   const int64_t units = n * segs, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
        un += step) {
-    const int64_t i = un / segs;
+    const int64_t i = item_row(un, segs);
     const int c0 = (int)(un - i * segs) * 32 * UNROLL + lane;
     const int64_t row = source_row(index, i, rows, status);
     uint2 q[UNROLL];
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(ROW_THREADS) load_rows(const uint8_t *__restri
   const int64_t units = n * nb, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
        un += step) {
-    const int64_t i = un / nb;
+    const int64_t i = item_row(un, nb);
     const int b = (int)(un - i * nb), j = b * BLOCK + lane;
     const int64_t row = source_row(index, i, rows, status);
     if (j < k)
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(ROW_THREADS) swiglu_save(const float *__restri
   const int64_t step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = lo * nb + (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32;
        un < hi * nb; un += step) {
-    const int64_t row = un / nb;
+    const int64_t row = item_row(un, nb);
     const int i = (int)(un - row * nb) * BLOCK + lane;
     const size_t at = (size_t)row * n + i;
     const float va = i < n ? a[at] : 0.0f, vu = i < n ? u[at] : 0.0f;
