@@ -137,6 +137,33 @@ moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void *dy, moe_d
                                float *dgate, void *ws, size_t ws_bytes, int32_t *dev_status,
                                moe_stream_t stream);
 
+/*
+ * Row lists of the experts' training pass for T tokens: the T * topk routed
+ * rows in the order of moe_dispatch_build, then, when n_shared is 1, one row
+ * per token for the shared expert, which becomes the last group.
+ *   offsets [n_routed + 1], sorted_token [T * topk], slot_of [T, topk] from
+ *   moe_dispatch_build, weights [T, topk] from moe_router_forward
+ *   row_token [R] int32, row_gate [R] fp32 out, R = T * (topk + n_shared):
+ *     the token of each row and its gate (1 for the shared expert)
+ *   group_offsets [n_routed + n_shared + 1] int32 out
+ * Limits: n_shared <= 1, R < 2^31.  A token or slot out of range is reported
+ * (MOE_ERR_RANGE) and not written.
+ */
+moe_status moe_training_rows(const moe_cfg *cfg, int64_t T, const int32_t *offsets,
+                             const int32_t *sorted_token, const int32_t *slot_of,
+                             const float *weights, int32_t *row_token, float *row_gate,
+                             int32_t *group_offsets, int32_t *dev_status, moe_stream_t stream);
+
+/*
+ * out[i,:] = src[index[i],:] for i < n, converted to out_dt (rounded once).
+ *   src [rows, k] of type dt, index [n] int32, out [n, k] of type out_dt
+ * An index outside [0, rows) gives a row of zeros and MOE_ERR_RANGE.
+ * Limits: rows, n < 2^31, k in [1, 2^20].
+ */
+moe_status moe_gather_rows(const void *src, moe_dtype dt, int64_t rows, int32_t k,
+                           const int32_t *index, int64_t n, void *out, moe_dtype out_dt,
+                           int32_t *dev_status, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,7 @@ the seeded input generator.
 """
 from .moe import (BlockParams, BlockShape, MoEBlock, combine, dispatch_build,  # noqa: F401
                   expert_weights_struct, experts_forward, router_forward, selftest_wait)
-from .training import (Checkpoint, checkpoint_rows, grouped_linear,  # noqa: F401
-                       grouped_linear_dw, grouped_linear_dx, restore_rows, swiglu_backward,
-                       swiglu_checkpoint)
+from .training import (Checkpoint, ExpertGrads, SavedExperts, checkpoint_rows,  # noqa: F401
+                       experts_training_backward, experts_training_forward, gather_rows,
+                       grouped_linear, grouped_linear_dw, grouped_linear_dx, restore_rows,
+                       swiglu_backward, swiglu_checkpoint, training_rows)

@@ -111,6 +111,10 @@ SIGNATURES = {
     ("moe_train", "moe_swiglu_backward"): (
         _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                _vp, _vp]),
+    ("moe_train", "moe_training_rows"): (
+        _i32, [_cfgp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("moe_train", "moe_gather_rows"): (
+        _i32, [_vp, _i32, _i64, _i32, _vp, _i64, _vp, _i32, _vp, _vp]),
 }
 
 LIBRARIES = ("moe_router", "moe_dispatch", "moe_experts", "moe_combine", "moe_train")

@@ -265,6 +265,72 @@ __global__ void __launch_bounds__(ROW_THREADS) load_rows(const uint8_t *__restri
   }
 }
 
+// ------------------------------------------------------------ plain rows
+
+// out[i] = src[index[i]], eight values a lane (VEC) or one.
+template <typename TI, typename TO, bool VEC>
+__global__ void __launch_bounds__(ROW_THREADS) gather_rows(const TI *__restrict__ src, int64_t rows,
+                                                           int k, const int32_t *__restrict__ index,
+                                                           int64_t n, TO *__restrict__ out,
+                                                           int32_t *status) {
+  constexpr int V = VEC ? 8 : 1, PER = 32 * UNROLL * V;  // values of an item
+  const int lane = threadIdx.x % 32, items = (k + PER - 1) / PER;
+  const int64_t units = n * items, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
+  for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
+       un += step) {
+    const int64_t i = item_row(un, items), row = source_row(index, i, rows, status);
+    const int c0 = (int)(un - i * items) * PER + lane * V;
+    float v[UNROLL][8];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int c = c0 + u * 32 * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[u][j] = 0.0f;
+      if (row >= 0 && c < k) {
+        if (VEC)
+          Vec8<TI>::load(src + row * k + c, v[u]);
+        else
+          v[u][0] = to_f(src[row * k + c]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int c = c0 + u * 32 * V;
+      if (c >= k) continue;
+      if (VEC)
+        Vec8<TO>::store(out + i * k + c, v[u]);
+      else
+        out[i * k + c] = from_f<TO>(v[u][0]);
+    }
+  }
+}
+
+// One thread per (token, slot), then one per shared row; the first threads
+// copy the group offsets.
+__global__ void __launch_bounds__(256) training_rows(const int32_t *__restrict__ offsets,
+                                                     const int32_t *__restrict__ sorted_token,
+                                                     const int32_t *__restrict__ slot_of,
+                                                     const float *__restrict__ weights, int64_t T,
+                                                     int k, int E, int shared, int32_t *row_token,
+                                                     float *row_gate, int32_t *group_offsets,
+                                                     int32_t *status) {
+  const int64_t routed = T * k, total = routed + (shared ? T : 0);
+  const int64_t step = (int64_t)gridDim.x * blockDim.x, me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  for (int64_t i = me; i < total; i += step) {
+    if (i >= routed) {
+      row_token[i] = (int32_t)(i - routed);
+      row_gate[i] = 1.0f;
+      continue;
+    }
+    const int32_t t = sorted_token[i], p = slot_of[i];
+    if (t < 0 || t >= T || p < 0 || p >= routed) set_status(status, MOE_ERR_RANGE);
+    if (t >= 0 && t < T) row_token[i] = t;
+    if (p >= 0 && p < routed) row_gate[p] = weights[i];
+  }
+  for (int64_t g = me; g <= E + shared; g += step)
+    group_offsets[g] = g <= E ? offsets[g] : (int32_t)total;
+}
+
 // ------------------------------------------- SwiGLU around the 8-bit format
 //
 // The elementwise halves of swiglu_checkpoint and swiglu_backward for the

@@ -363,8 +363,8 @@ MOE_EXPORT moe_status moe_grouped_linear_dx(const moe_grouped_shape *s, const vo
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
   if (!act_type(dt) || !act_type(dx_dt)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0) return MOE_OK;  // (an empty dy2 may well be NULL)
   if ((dy2 == nullptr) != (w2 == nullptr)) return MOE_ERR_INVALID;
-  if (s->rows == 0) return MOE_OK;
   if (!dy || !w || !offsets || !dx) return MOE_ERR_INVALID;
   return run_dx({s, dt, dx_dt, dy, w, dy2, w2, offsets, dx, 0, dev_status, as_stream(stream)});
 }
@@ -541,5 +541,62 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
     ckpt::swiglu_grads<<<grid, ckpt::ROW_THREADS, 0, cs>>>(
         dh, sv, gate, offsets, s->groups, s->rows, s->n, static_cast<bf16 *>(da),
         static_cast<bf16 *>(du), static_cast<bf16 *>(hg), dgate);
+  return launch_status();
+}
+
+MOE_EXPORT moe_status moe_training_rows(const moe_cfg *cfg, int64_t T, const int32_t *offsets,
+                                        const int32_t *sorted_token, const int32_t *slot_of,
+                                        const float *weights, int32_t *row_token, float *row_gate,
+                                        int32_t *group_offsets, int32_t *dev_status,
+                                        moe_stream_t stream) {
+  const moe_status st = check_cfg(cfg);
+  if (st != MOE_OK) return st;
+  if (T < 0) return MOE_ERR_INVALID;
+  if (cfg->n_shared > 1 || T * ((int64_t)cfg->topk + cfg->n_shared) >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (!offsets || !group_offsets) return MOE_ERR_INVALID;
+  if (T > 0 && (!sorted_token || !slot_of || !weights || !row_token || !row_gate))
+    return MOE_ERR_INVALID;
+  const int64_t items = T * (cfg->topk + cfg->n_shared) + cfg->n_routed + 2;
+  const int64_t blocks = (items + 255) / 256;
+  ckpt::training_rows<<<(unsigned)(blocks < 1184 ? blocks : 1184), 256, 0, as_stream(stream)>>>(
+      offsets, sorted_token, slot_of, weights, T, cfg->topk, cfg->n_routed, cfg->n_shared, row_token,
+      row_gate, group_offsets, dev_status);
+  return launch_status();
+}
+
+template <typename TI, typename TO>
+static void launch_gather(bool vec, unsigned grid, const void *src, int64_t rows, int32_t k,
+                          const int32_t *index, int64_t n, void *out, int32_t *status,
+                          cudaStream_t s) {
+  if (vec)
+    ckpt::gather_rows<TI, TO, true><<<grid, ckpt::ROW_THREADS, 0, s>>>(
+        static_cast<const TI *>(src), rows, k, index, n, static_cast<TO *>(out), status);
+  else
+    ckpt::gather_rows<TI, TO, false><<<grid, ckpt::ROW_THREADS, 0, s>>>(
+        static_cast<const TI *>(src), rows, k, index, n, static_cast<TO *>(out), status);
+}
+
+MOE_EXPORT moe_status moe_gather_rows(const void *src, moe_dtype dt, int64_t rows, int32_t k,
+                                      const int32_t *index, int64_t n, void *out, moe_dtype out_dt,
+                                      int32_t *dev_status, moe_stream_t stream) {
+  if (rows < 0 || n < 0 || k < 1) return MOE_ERR_INVALID;
+  if (rows >= ((int64_t)1 << 31) || n >= ((int64_t)1 << 31) || k > (1 << 20) || !act_type(dt) ||
+      !act_type(out_dt))
+    return MOE_ERR_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (!index || !out || (rows > 0 && !src)) return MOE_ERR_INVALID;
+  const bool vec = k % 8 == 0 && aligned(src, 16) && aligned(out, 16);
+  const int per = 32 * ckpt::UNROLL * (vec ? 8 : 1);
+  const unsigned grid = row_grid(n * ((k + per - 1) / per));
+  cudaStream_t cs = as_stream(stream);
+  if (dt == MOE_F32 && out_dt == MOE_F32)
+    launch_gather<float, float>(vec, grid, src, rows, k, index, n, out, dev_status, cs);
+  else if (dt == MOE_F32)
+    launch_gather<float, bf16>(vec, grid, src, rows, k, index, n, out, dev_status, cs);
+  else if (out_dt == MOE_F32)
+    launch_gather<bf16, float>(vec, grid, src, rows, k, index, n, out, dev_status, cs);
+  else
+    launch_gather<bf16, bf16>(vec, grid, src, rows, k, index, n, out, dev_status, cs);
   return launch_status();
 }

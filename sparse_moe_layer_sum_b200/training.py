@@ -11,6 +11,13 @@ synchronise; rows outside the groups are left as they were.
     dw = grouped_linear_dw(dy, x, offsets)                # dw = dy^T x
     h, a, u = swiglu_checkpoint(x, w1, w3, offsets)       # a, u kept in 8 bits
     da, du, hg, dgate = swiglu_backward(dy, w2, a, u, offsets, gate=gate)
+
+Together they train the experts of a block on the routing of a batch:
+
+    weights, indices, _ = router_forward(shape, x, w_r, bias)
+    _, offsets, sorted_token, slot_of = dispatch_build(shape, indices)
+    y, saved = experts_training_forward(shape, params, x, weights, offsets, sorted_token, slot_of)
+    grads = experts_training_backward(shape, params, saved, dy)
 """
 from __future__ import annotations
 
@@ -22,7 +29,7 @@ import torch
 
 from . import _lib
 from ._lib import MoEGroupedShape, check, fn
-from .moe import _ptr
+from .moe import BlockParams, BlockShape, _ptr, combine
 
 _DT = {torch.float32: _lib.DTYPES["f32"], torch.bfloat16: _lib.DTYPES["bf16"]}
 SCALE_BLOCK = 32  # values of a row that share a scale
@@ -271,3 +278,132 @@ def swiglu_backward(dy: torch.Tensor, w2: torch.Tensor, a: Checkpoint, u: Checkp
           offsets.data_ptr(), da.data_ptr(), du.data_ptr(), hg.data_ptr(), dgate.data_ptr(),
           _ptr(ws), 0 if ws is None else ws.numel(), _status(status))
     return da, du, hg, dgate
+
+
+def gather_rows(src: torch.Tensor, index: torch.Tensor, *, dtype: Optional[torch.dtype] = None,
+                status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_gather_rows: src[index] for src [rows, k] and index [n] int32, in
+    `dtype` (src's own without)."""
+    dev = _check(src, index, status)
+    _need(src.dim() == 2 and index.dtype == torch.int32 and index.dim() == 1,
+          "src must be [rows, k] and index int32 [n]")
+    dt = _dtype(src)
+    (rows, k), n = src.shape, index.numel()
+    out = _out(None, (n, k), dtype or src.dtype, dev)
+    _call(dev, "moe_gather_rows", src.data_ptr(), dt, rows, k, index.data_ptr(), n, out.data_ptr(),
+          _DT[out.dtype], _status(status))
+    return out
+
+
+def training_rows(shape: BlockShape, weights: torch.Tensor, offsets: torch.Tensor,
+                  sorted_token: torch.Tensor, slot_of: torch.Tensor, *,
+                  status: Optional[torch.Tensor] = None):
+    """moe_training_rows: (row_token, row_gate, group_offsets) of a batch's
+    routed rows followed by the shared expert's."""
+    dev = _check(weights, offsets, sorted_token, slot_of, status)
+    T, k = weights.shape
+    _need(k == shape.topk and weights.dtype == torch.float32, "weights must be fp32 [T, topk]")
+    _need(offsets.dtype == sorted_token.dtype == slot_of.dtype == torch.int32
+          and offsets.numel() == shape.n_routed + 1
+          and sorted_token.numel() == slot_of.numel() == T * k,
+          "offsets, sorted_token and slot_of must be dispatch_build's")
+    R = T * (k + shape.n_shared)
+    row_token = torch.empty(R, dtype=torch.int32, device=dev)
+    row_gate = torch.empty(R, dtype=torch.float32, device=dev)
+    group_offsets = torch.empty(shape.n_routed + shape.n_shared + 1, dtype=torch.int32, device=dev)
+    cfg = shape.cfg()
+    _call(dev, "moe_training_rows", ctypes.byref(cfg), T, offsets.data_ptr(), sorted_token.data_ptr(),
+          slot_of.data_ptr(), weights.data_ptr(), row_token.data_ptr(), row_gate.data_ptr(),
+          group_offsets.data_ptr(), _status(status))
+    return row_token, row_gate, group_offsets
+
+
+@dataclass
+class SavedExperts:
+    """What experts_training_forward leaves for the backward pass: the batch
+    and the two projections in 8 bits, and the routing's row lists."""
+
+    x: Checkpoint
+    a: Checkpoint
+    u: Checkpoint
+    row_token: torch.Tensor
+    row_gate: torch.Tensor
+    group_offsets: torch.Tensor
+    slot_of: torch.Tensor
+    dtype: torch.dtype
+
+    @property
+    def nbytes(self) -> int:
+        return self.x.nbytes + self.a.nbytes + self.u.nbytes
+
+
+@dataclass
+class ExpertGrads:
+    """Gradients of one batch: dx [T, dim] fp32 (through the experts; the
+    router's share is not in it), dgates [T, topk] fp32, and the weights'
+    gradients, stacked as the weights are."""
+
+    dx: torch.Tensor
+    dgates: torch.Tensor
+    dw1: torch.Tensor
+    dw3: torch.Tensor
+    dw2: torch.Tensor
+
+
+def _token_sums(shape: BlockShape, weights, slot_of, rows, status) -> torch.Tensor:
+    """moe_combine of the routed rows, then the shared expert's."""
+    n = weights.numel()
+    with torch.cuda.device(rows.device):
+        return combine(shape, weights, slot_of, rows[:n], rows[n:] if shape.n_shared else None,
+                       status=status)
+
+
+def experts_training_forward(shape: BlockShape, params: BlockParams, x: torch.Tensor,
+                             weights: torch.Tensor, offsets: torch.Tensor,
+                             sorted_token: torch.Tensor, slot_of: torch.Tensor, *,
+                             status: Optional[torch.Tensor] = None):
+    """(y [T, dim] fp32, SavedExperts) of the routed experts and the shared one
+    for x [T, dim], with the routing of router_forward and dispatch_build.
+    Weights in x's dtype (bf16 or fp32).  y is the ordered sum of moe_combine,
+    bit-reproducible."""
+    _need(x.dim() == 2 and x.shape[1] == shape.dim, "x must be [T, dim]")
+    _need(params.w1.dtype == x.dtype and x.dtype in _DT, "training takes weights in x's dtype")
+    T, k = x.shape[0], shape.topk
+    row_token, row_gate, group_offsets = training_rows(shape, weights, offsets, sorted_token, slot_of,
+                                                       status=status)
+    rows = gather_rows(x, row_token, status=status)
+    h, a, u = swiglu_checkpoint(rows, params.w1, params.w3, group_offsets, status=status)
+    o = grouped_linear(h, params.w2, group_offsets, out_dtype=torch.float32, status=status)
+    y = _token_sums(shape, weights, slot_of, o, status)
+    return y, SavedExperts(checkpoint_rows(x), a, u, row_token, row_gate, group_offsets, slot_of,
+                           x.dtype)
+
+
+def experts_training_backward(shape: BlockShape, params: BlockParams, saved: SavedExperts,
+                              dy: torch.Tensor, *, grad_dtype: torch.dtype = torch.float32,
+                              accumulate: Optional[ExpertGrads] = None,
+                              status: Optional[torch.Tensor] = None) -> ExpertGrads:
+    """Gradients of experts_training_forward for dy [T, dim] (fp32 or the
+    weights' dtype).  With `accumulate` the weights' gradients are added to its
+    dw1, dw3 and dw2; otherwise they are new tensors of grad_dtype."""
+    T, k = saved.x.codes.shape[0], shape.topk
+    _need(tuple(dy.shape) == (T, shape.dim), "dy must be [T, dim]")
+    st = dict(status=status)
+    off = saved.group_offsets
+    dyr = gather_rows(dy, saved.row_token, dtype=saved.dtype, **st)
+    da, du, hg, dgate = swiglu_backward(dyr, params.w2, saved.a, saved.u, off, gate=saved.row_gate, **st)
+
+    def dw(d, rows, name):
+        out = getattr(accumulate, name) if accumulate is not None else None
+        return grouped_linear_dw(d, rows, off, out=out, out_dtype=None if out is not None else grad_dtype,
+                                 accumulate=out is not None, **st)
+
+    dw2 = dw(dyr, hg, "dw2")
+    rows = restore_rows(saved.x, saved.row_token, dtype=saved.dtype, **st)
+    dw1, dw3 = dw(da, rows, "dw1"), dw(du, rows, "dw3")
+    dxr = grouped_linear_dx(da, params.w1, off, dy2=du, w2=params.w3, out_dtype=torch.float32, **st)
+    # the tokens' rows summed in slot order, the shared expert's last
+    ones = torch.ones(T, k, dtype=torch.float32, device=dy.device)
+    dx = _token_sums(shape, ones, saved.slot_of, dxr, status)
+    dgates = gather_rows(dgate[:T * k].view(-1, 1), saved.slot_of.view(-1), **st).view(T, k)
+    return ExpertGrads(dx, dgates, dw1, dw3, dw2)

@@ -131,3 +131,22 @@ def test_reference_gradients_against_autograd():
     for got, want in zip(vals, (a.grad, u.grad, None, gate.grad)):
         if want is not None:
             assert (got - want).abs().max() < 1e-12
+
+
+def test_training_rows_and_gather_refusals():
+    from sparse_moe_layer_sum_b200._lib import MoECfg
+    f, g = fn("moe_train", "moe_training_rows"), fn("moe_train", "moe_gather_rows")
+    cfg = lambda **kw: ctypes.byref(MoECfg(*{**dict(
+        dim=256, n_routed=16, n_groups=4, topk_groups=2, topk=4, inter=128, n_shared=1,
+        route_scale=2.5, score_func=0, has_bias=1), **kw}.values()))
+    call = lambda c, T=4, off=P, tok=P, out=P: f(c, T, off, tok, P, P, out, P, P, None, None)
+    assert call(None) == INVALID and call(cfg(topk=0)) == INVALID and call(cfg(), T=-1) == INVALID
+    assert call(cfg(n_shared=2)) == UNSUPPORTED and call(cfg(), T=1 << 29) == UNSUPPORTED
+    assert call(cfg(), off=None) == INVALID and call(cfg(), tok=None) == INVALID
+    assert call(cfg(), out=None) == INVALID
+    assert g(P, BF16, 4, 8, None, 2, P, BF16, None, None) == INVALID
+    assert g(P, BF16, 4, 0, P, 2, P, BF16, None, None) == INVALID
+    assert g(None, BF16, 4, 8, P, 2, P, BF16, None, None) == INVALID
+    assert g(P, E4M3, 4, 8, P, 2, P, BF16, None, None) == UNSUPPORTED
+    assert g(P, BF16, 1 << 31, 8, P, 2, P, BF16, None, None) == UNSUPPORTED
+    assert g(None, BF16, 4, 8, None, 0, None, BF16, None, None) == 0
