@@ -21,9 +21,15 @@
  *  - Operands are MOE_BF16 or MOE_F32, both operands of a product the same.
  *    Sums are fp32 and rounded once at the end.
  *  - No atomics: results do not depend on the order in which blocks run.
- *  - bf16 operands run on the tcgen05 tensor cores when the rows of every
- *    operand are multiples of 16 bytes and every operand is 16-byte aligned;
- *    everything else runs on the CUDA cores with fp32 multiply-adds.
+ *  - bf16 operands whose rows are multiples of 16 bytes and whose addresses
+ *    are 16-byte aligned run on the tcgen05 tensor cores as they are.  Other
+ *    products of some size do through copies in the workspace: bf16 rows
+ *    padded, fp32 operands split into three bf16 terms (results as exact as
+ *    fp32 sums; a result that depends on an infinite fp32 operand may be NaN).
+ *    Small ones, and any without a workspace, run on the CUDA cores with fp32
+ *    multiply-adds.
+ *  - Each *_workspace_size takes `aligned`: 1 when every operand of the call
+ *    is 16-byte aligned, as fresh allocations are; 0 asks for enough for any.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H
@@ -42,13 +48,18 @@ typedef struct {
 /*
  * y[p,:] = x[p,:] w[g]^T for every row p of every group g.
  *   x [rows, k], w [groups, n, k] of type dt; y [rows, n] of type y_dt
+ *   ws  moe_grouped_linear_workspace_size bytes, 16-byte aligned; may be NULL
+ *       (then the CUDA cores do what would have been copied)
  * Rows of y outside the groups are left as they were.
  * Device errors: MOE_ERR_RANGE (offsets), MOE_ERR_TIMEOUT (a pipeline wait
  * expired; outputs unspecified).  The same for the calls below.
  */
+size_t moe_grouped_linear_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                         int32_t aligned);
 moe_status moe_grouped_linear(const moe_grouped_shape *s, const void *x, moe_dtype dt,
                               const void *w, const int32_t *offsets, void *y, moe_dtype y_dt,
-                              int32_t *dev_status, moe_stream_t stream);
+                              void *ws, size_t ws_bytes, int32_t *dev_status,
+                              moe_stream_t stream);
 
 /*
  * The input gradient: dx[p,:] = dy[p,:] w[g] (+ dy2[p,:] w2[g]).
@@ -56,10 +67,12 @@ moe_status moe_grouped_linear(const moe_grouped_shape *s, const void *x, moe_dty
  * dy2 and w2 (both or neither NULL) add a second product in the same fp32
  * sum: w1 and w3 share their input, so its gradient is the sum of two.
  */
+size_t moe_grouped_linear_dx_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                            int32_t two, int32_t aligned); /* two: with dy2 */
 moe_status moe_grouped_linear_dx(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
                                  const void *w, const void *dy2, const void *w2,
-                                 const int32_t *offsets, void *dx, moe_dtype dx_dt,
-                                 int32_t *dev_status, moe_stream_t stream);
+                                 const int32_t *offsets, void *dx, moe_dtype dx_dt, void *ws,
+                                 size_t ws_bytes, int32_t *dev_status, moe_stream_t stream);
 
 /*
  * The weight gradient: dw[g] = sum over the rows p of group g of
@@ -68,10 +81,12 @@ moe_status moe_grouped_linear_dx(const moe_grouped_shape *s, const void *dy, moe
  * A group without rows has a zero gradient (accumulate 0) or leaves its part
  * of dw as it was (accumulate 1).
  */
+size_t moe_grouped_linear_dw_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                            int32_t aligned);
 moe_status moe_grouped_linear_dw(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
                                  const void *x, const int32_t *offsets, void *dw,
-                                 moe_dtype dw_dt, int32_t accumulate, int32_t *dev_status,
-                                 moe_stream_t stream);
+                                 moe_dtype dw_dt, int32_t accumulate, void *ws, size_t ws_bytes,
+                                 int32_t *dev_status, moe_stream_t stream);
 
 /*
  * The 8-bit format: a row of k values is stored as k e4m3 codes and
@@ -102,9 +117,8 @@ moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps, int64_t r
  * straight from their fp32 sums (s->n is the hidden width, s->k the model's).
  *   x [rows, k], w1, w3 [groups, n, k] of type dt; h [rows, n] of type dt
  *   codes_a, codes_u [rows, n], exps_a, exps_u [rows, ceil(n / 32)] uint8
- *   ws  moe_swiglu_checkpoint_workspace_size bytes (0: ws may be NULL).
- *       aligned: 1 when x, w1, w3, h and the codes are all 16-byte aligned,
- *       as fresh allocations are; 0 asks for enough for any operands.
+ *   ws  moe_swiglu_checkpoint_workspace_size bytes, 16-byte aligned (NULL if
+ *       that is 0); operands: x, w1, w3
  */
 size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
                                             int32_t aligned);
@@ -125,8 +139,8 @@ moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const void *x, moe_
  * hg is the operand of w2's gradient, grouped_linear_dw(dy, hg).
  *   dy [rows, k], w2 [groups, k, n] of type dt (s->n the hidden width)
  *   gate [rows] fp32 or NULL (1); da, du, hg [rows, n]; dgate [rows] fp32
- *   ws  moe_swiglu_backward_workspace_size bytes; aligned as above, for dy,
- *       w2, the codes, da, du and hg
+ *   ws  moe_swiglu_backward_workspace_size bytes, 16-byte aligned; operands:
+ *       dy, w2
  */
 size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
                                           int32_t aligned);

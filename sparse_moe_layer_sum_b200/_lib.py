@@ -96,11 +96,14 @@ SIGNATURES = {
     ("moe_experts", "moe_experts_selftest_wait"): (_i32, [_i64, _vp, _vp]),
     ("moe_combine", "moe_combine"): (_i32, [_cfgp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     ("moe_train", "moe_grouped_linear"): (
-        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp, _vp]),
+    ("moe_train", "moe_grouped_linear_workspace_size"): (_sz, [_gsp, _i32, _i32]),
+    ("moe_train", "moe_grouped_linear_dx_workspace_size"): (_sz, [_gsp, _i32, _i32, _i32]),
+    ("moe_train", "moe_grouped_linear_dw_workspace_size"): (_sz, [_gsp, _i32, _i32]),
     ("moe_train", "moe_grouped_linear_dx"): (
-        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp, _vp]),
     ("moe_train", "moe_grouped_linear_dw"): (
-        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp]),
+        _i32, [_gsp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _sz, _vp, _vp]),
     ("moe_train", "moe_checkpoint_rows"): (_i32, [_vp, _i32, _i64, _i32, _vp, _vp, _vp]),
     ("moe_train", "moe_restore_rows"): (
         _i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _vp, _vp]),

@@ -16,6 +16,15 @@
 //   rows behind it are zeroed in shared memory up to the next multiple of 16
 //   (both operands: the next group may hold infinities), and the MMAs beyond
 //   are not issued.
+//
+// Operands that TMA cannot read or the MMA cannot multiply are staged first
+// (stage_rows): bf16 rows off the 16-byte pitch are copied to padded rows, and
+// fp32 operands are split into three bf16 terms, x = x0 + x1 + x2 with 8 bits
+// of the significand each.  Of the nine products of two split operands the six
+// down to 2^-16 are multiplied, smallest first, as six passes over the
+// contraction into the same sums; what is left out is within 2^-25 of a
+// product.  fp32 products run at a sixth of the bf16 rate that way, still
+// several times the CUDA cores' rate.
 #pragma once
 
 #include <cuda.h>
@@ -172,6 +181,45 @@ __device__ __forceinline__ uint8_t *align_smem(uint8_t *raw) {
                                      ~static_cast<uintptr_t>(1023));
 }
 
+// -------------------------------------------------------------------- staging
+
+constexpr int SPLIT_TERMS = 3, SPLIT_PASSES = 6;
+
+// Terms of the two operands that pass q multiplies, smallest products first.
+__device__ __forceinline__ int term_a(int q) { return (0x118 >> (2 * q)) & 3; }  // 0 2 1 0 1 0
+__device__ __forceinline__ int term_b(int q) { return (0x052 >> (2 * q)) & 3; }  // 2 0 1 1 0 0
+
+// src [rows, k] into TERMS planes [rows, kp] of bf16, kp = k rounded up to 8,
+// zeros behind k.  One term is a copy (rounded, for fp32 src).  A value that is
+// not finite, or rounds to infinity, stays in the first term alone.
+template <typename TI, int TERMS>
+__global__ void __launch_bounds__(256) stage_rows(const TI *__restrict__ src, int64_t rows, int k,
+                                                  int kp, bf16 *__restrict__ dst) {
+  const int64_t per = kp / 8, total = rows * per, plane = rows * kp;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = ckpt::item_row(i, (int)per);
+    const int c = (int)(i - r * per) * 8;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < k ? to_f(src[r * k + c + j]) : 0.0f;
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j], v[j + 1]);
+        w[j / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        if (t + 1 < TERMS) {
+          const float2 f = __bfloat1622float2(h);
+          v[j] = isfinite(f.x) ? v[j] - f.x : 0.0f;  // exact
+          v[j + 1] = isfinite(f.y) ? v[j + 1] - f.y : 0.0f;
+        }
+      }
+      *reinterpret_cast<uint4 *>(dst + t * plane + r * kp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // ----------------------------------------------------------------- rows_gemm
 
 enum Op { LIN, DX, UP, BWD };
@@ -179,13 +227,15 @@ enum Op { LIN, DX, UP, BWD };
 struct RowParams {
   const int32_t *offsets;
   int G, F;          // F: features (columns of the result)
-  int kb0, kb;       // k-blocks of the first source, of all sources
+  int kb0, kb;       // k-blocks of one pass, of all passes of all sources
+  int passes;        // 1, or SPLIT_PASSES for split operands
+  int vec;           // UP, BWD: rows of the results in whole vectors of 4
   int64_t rows;
   void *out;         // LIN, DX: [rows, F]; UP: h
   int32_t *status;
   ckpt::Saved saved;  // UP: written; BWD: read
   const float *gate;  // BWD, may be NULL
-  bf16 *da, *du, *hg;
+  void *da, *du, *hg;
   float *part;        // BWD: [ceil(F / 32), rows] terms of dgate
 };
 
@@ -266,8 +316,53 @@ __device__ __forceinline__ void finish_packed(const RowParams &p, const uint32_t
 // rolled loop (straight-line code for 128 sums per lane stalled on
 // instruction fetches).  x: [rows][32 features] of this warp.
 
+template <typename T>
+__device__ __forceinline__ void put4(void *base, size_t at, const float (&v)[4], int left, bool vec);
+template <>
+__device__ __forceinline__ void put4<bf16>(void *base, size_t at, const float (&v)[4], int left, bool vec) {
+  bf16 *o = static_cast<bf16 *>(base) + at;
+  if (vec) {
+    *reinterpret_cast<uint2 *>(o) = make_uint2(pack(v[0], v[1]), pack(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) o[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void put4<float>(void *base, size_t at, const float (&v)[4], int left, bool vec) {
+  float *o = static_cast<float *>(base) + at;
+  if (vec) {
+    *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) o[i] = v[i];
+  }
+}
+__device__ __forceinline__ void put4_codes(uint8_t *o, const float (&v)[4], float inv, int left, bool vec) {
+  const uint32_t w = (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(v[0], inv), ckpt::scaled(v[1], inv)) |
+                     (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(v[2], inv), ckpt::scaled(v[3], inv)) << 16;
+  if (vec) {
+    *reinterpret_cast<uint32_t *>(o) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) o[i] = (uint8_t)(w >> (8 * i));
+  }
+}
+__device__ __forceinline__ uint32_t get4_codes(const uint8_t *q, int left, bool vec) {
+  if (vec) return __ldg(reinterpret_cast<const uint32_t *>(q));
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) w |= (uint32_t)__ldg(q + i) << (8 * i);
+  return w;
+}
+
 // 8 rows of a and u.  The 32 features are one scale block, so its largest
 // magnitude is a reduction over the 8 lanes of a row.
+template <typename TO>
 __device__ __forceinline__ void finish_up(const RowParams &p, const float *x, int fw, int row0,
                                           int nv) {
   const int lane = threadIdx.x % 32, f = fw + lane % 8 * 4;
@@ -294,15 +389,11 @@ __device__ __forceinline__ void finish_up(const RowParams &p, const float *x, in
     const float ia = ckpt::inv_scale_of(ea), iu = ckpt::inv_scale_of(eu);
     float h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = a[i] * ckpt::sigmoid<bf16>(a[i]) * u[i];
+    for (int i = 0; i < 4; ++i) h[i] = a[i] * ckpt::sigmoid<TO>(a[i]) * u[i];
     const size_t at = (size_t)(row0 + r) * p.F + f;
-    *reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + at) = make_uint2(pack(h[0], h[1]), pack(h[2], h[3]));
-    *reinterpret_cast<uint32_t *>(p.saved.ca + at) =
-        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(a[0], ia), ckpt::scaled(a[1], ia)) |
-        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(a[2], ia), ckpt::scaled(a[3], ia)) << 16;
-    *reinterpret_cast<uint32_t *>(p.saved.cu + at) =
-        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(u[0], iu), ckpt::scaled(u[1], iu)) |
-        (uint32_t)f32x2_to_e4m3x2(ckpt::scaled(u[2], iu), ckpt::scaled(u[3], iu)) << 16;
+    put4<TO>(p.out, at, h, p.F - f, p.vec);
+    put4_codes(p.saved.ca + at, a, ia, p.F - f, p.vec);
+    put4_codes(p.saved.cu + at, u, iu, p.F - f, p.vec);
     if (lane % 8 == 0) {
       const size_t sat = (size_t)(row0 + r) * nb + fw / ckpt::BLOCK;
       p.saved.ea[sat] = (uint8_t)ea;
@@ -327,8 +418,8 @@ struct BwdRows {
       g[s] = 1.0f;
       if (r < nv && f < p.F) {
         const size_t at = (size_t)(row0 + r) * p.F + f, sat = (size_t)(row0 + r) * nb + fw / ckpt::BLOCK;
-        ca[s] = __ldg(reinterpret_cast<const uint32_t *>(p.saved.ca + at));
-        cu[s] = __ldg(reinterpret_cast<const uint32_t *>(p.saved.cu + at));
+        ca[s] = get4_codes(p.saved.ca + at, p.F - f, p.vec);
+        cu[s] = get4_codes(p.saved.cu + at, p.F - f, p.vec);
         e[s] = __ldg(p.saved.ea + sat) | __ldg(p.saved.eu + sat) << 8;
         if (p.gate) g[s] = __ldg(p.gate + row0 + r);
       }
@@ -336,6 +427,7 @@ struct BwdRows {
   }
 };
 
+template <typename TO>
 __device__ __forceinline__ void finish_bwd(const RowParams &p, const BwdRows &in, const float *x, int fw,
                                            int row0, int nv) {
   const int lane = threadIdx.x % 32, f = fw + lane % 8 * 4;
@@ -349,18 +441,18 @@ __device__ __forceinline__ void finish_bwd(const RowParams &p, const BwdRows &in
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       const float2 a = ckpt::decode2((uint16_t)(in.ca[s] >> (8 * i))), u = ckpt::decode2((uint16_t)(in.cu[s] >> (8 * i)));
-      term += ckpt::swiglu_grad<bf16>(a.x * sa, u.x * su, dh[i], in.g[s], da[i], du[i], hg[i]);
-      term += ckpt::swiglu_grad<bf16>(a.y * sa, u.y * su, dh[i + 1], in.g[s], da[i + 1], du[i + 1], hg[i + 1]);
+      const float t0 = ckpt::swiglu_grad<TO>(a.x * sa, u.x * su, dh[i], in.g[s], da[i], du[i], hg[i]);
+      const float t1 = ckpt::swiglu_grad<TO>(a.y * sa, u.y * su, dh[i + 1], in.g[s], da[i + 1], du[i + 1], hg[i + 1]);
+      if (r < nv && f + i < p.F) term += t0;
+      if (r < nv && f + i + 1 < p.F) term += t1;
     }
-    const bool on = r < nv && f < p.F;
-    if (!on) term = 0.0f;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-    if (!on) continue;
+    if (r >= nv || f >= p.F) continue;
     const size_t at = (size_t)(row0 + r) * p.F + f;
-    *reinterpret_cast<uint2 *>(p.da + at) = make_uint2(pack(da[0], da[1]), pack(da[2], da[3]));
-    *reinterpret_cast<uint2 *>(p.du + at) = make_uint2(pack(du[0], du[1]), pack(du[2], du[3]));
-    *reinterpret_cast<uint2 *>(p.hg + at) = make_uint2(pack(hg[0], hg[1]), pack(hg[2], hg[3]));
+    put4<TO>(p.da, at, da, p.F - f, p.vec);
+    put4<TO>(p.du, at, du, p.F - f, p.vec);
+    put4<TO>(p.hg, at, hg, p.F - f, p.vec);
     if (lane % 8 == 0) p.part[(size_t)(fw / ckpt::BLOCK) * p.rows + row0 + r] = term;
   }
 }
@@ -446,8 +538,8 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
         // tiles that run together start at different k-blocks, which spreads
         // their reads of shared operands over L2
         const int k0 = (t.ft * 7 + t.tt * 5) % p.kb;
+        int q = k0 / p.kb0, blk = k0 - q * p.kb0;  // pass (of all sources) and block of it
         for (int i = 0; i < p.kb; ++i) {
-          const int kb = k0 + i < p.kb ? k0 + i : k0 + i - p.kb;
           if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
             ok = false;
             break;
@@ -457,21 +549,28 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
           pending[r.stage] = (int)r.phase;
           uint8_t *a = sm + r.stage * C::STAGE, *b = a + C::A_ALL;
           const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(full + r.stage), 0) : smem_u32(full + r.stage);
-          const bool second = kb >= p.kb0;
-          const int kk = (second ? kb - p.kb0 : kb) * BK;
+          const bool second = q >= p.passes;
+          const int kk = blk * BK;
+          const int term = p.passes == 1 ? SPLIT_PASSES - 1 : second ? q - p.passes : q;
+          const int za = term_a(term) * p.G + t.g;                    // plane of the weights
+          const int yb = term_b(term) * (int)p.rows + b0;             // row of the row planes
+          if (++blk == p.kb0) {
+            blk = 0;
+            if (++q * p.kb0 == p.kb) q = 0;
+          }
           const CUtensorMap *ma = second ? &tmA1 : &tmA0, *mb = second ? &tmB1 : &tmB0;
 #pragma unroll
           for (int i2 = 0; i2 < AT; ++i2) {
             const int f = f0 + (OP == UP ? 0 : i2 * BM * CG);
             if (C::KMAJOR) {
-              load_3d<CG>(OP == UP && i2 == 1 ? &tmA1 : ma, a + i2 * TILE, bar, kk, f, t.g, pol_a);
+              load_3d<CG>(OP == UP && i2 == 1 ? &tmA1 : ma, a + i2 * TILE, bar, kk, f, za, pol_a);
             } else {
-              load_3d<CG>(ma, a + i2 * TILE, bar, f, kk, t.g, pol_a);
-              load_3d<CG>(ma, a + i2 * TILE + BOX, bar, f + 64, kk, t.g, pol_a);
+              load_3d<CG>(ma, a + i2 * TILE, bar, f, kk, za, pol_a);
+              load_3d<CG>(ma, a + i2 * TILE + BOX, bar, f + 64, kk, za, pol_a);
             }
           }
           for (int j = 0; j < nbox; ++j)
-            load_2d<CG>(mb, b + j * C::BOXN * BK * 2, bar, kk, b0 + j * C::BOXN, pol_b);
+            load_2d<CG>(mb, b + j * C::BOXN * BK * 2, bar, kk, yb + j * C::BOXN, pol_b);
           r.next(STAGES);
         }
       }
@@ -615,9 +714,9 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
               }
             __syncwarp();
             if (OP == UP)
-              finish_up(p, x, fw, t.row0 + c0, t.nvalid - c0);
+              finish_up<TO>(p, x, fw, t.row0 + c0, t.nvalid - c0);
             else
-              finish_bwd(p, in, x, fw, t.row0 + c0, t.nvalid - c0);
+              finish_bwd<TO>(p, in, x, fw, t.row0 + c0, t.nvalid - c0);
           }
         } else {
 #pragma unroll
@@ -704,6 +803,8 @@ struct DwParams {
   int64_t rows;
   void *dw;
   int accumulate;
+  int passes;     // 1, or SPLIT_PASSES for split operands
+  int tma_store;  // rows of dw are multiples of 16 bytes, dw is 16-byte aligned
   int32_t *status;
 };
 
@@ -778,10 +879,12 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
   const int64_t total = (int64_t)p.G * ntiles * ktiles;
 
   struct Job {
-    int g, n0, k0, lo, kc, kb, tail;  // kb: k-blocks; tail: rows of the last one
-    int nmma;                         // columns of the MMA
-    // whether k-block i ends inside a 16-row step
-    __device__ __forceinline__ bool fix(int i) const { return i == kb - 1 && tail % 16 != 0; }
+    int g, n0, k0, lo, kc;
+    int kb0, kb, tail;  // k-blocks of one pass and of all; rows of a pass's last one
+    int nmma;           // columns of the MMA
+    // rows of k-block b of a pass, and whether it ends inside a 16-row step
+    __device__ __forceinline__ int depth(int b) const { return b == kb0 - 1 ? tail : BK; }
+    __device__ __forceinline__ bool fix(int b) const { return depth(b) % 16 != 0; }
   };
   auto job = [&](int64_t tile) {
     Job j;
@@ -790,8 +893,9 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     j.n0 = local / ktiles * C::FEAT;
     j.k0 = local % ktiles * 256;
     group_bounds(p.offsets, j.g, p.rows, j.lo, j.kc, threadIdx.x == 0 ? p.status : nullptr);
-    j.kb = (j.kc + BK - 1) / BK;
-    j.tail = j.kc - (j.kb - 1) * BK;
+    j.kb0 = (j.kc + BK - 1) / BK;
+    j.kb = j.kb0 * p.passes;
+    j.tail = j.kc - (j.kb0 - 1) * BK;
     j.nmma = min(256, (p.k - j.k0 + 31) / 32 * 32);
     return j;
   };
@@ -809,6 +913,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
         const int hb = j.nmma / 2, nbox = (hb + 63) / 64;
         const int n0 = j.n0 + (int)rank * BM, k0 = j.k0 + (int)rank * hb;
         const uint32_t bytes = (uint32_t)(AT * TILE + nbox * BOX);
+        int q = 0, blk = 0;  // pass and block of it
         for (int i = 0; i < j.kb; ++i) {
           if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
             ok = false;
@@ -816,7 +921,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
           }
           // a last block that ends inside a 16-row step is completed on each
           // SM's own `tail` barrier and handed on when its rows are zeroed
-          const bool fix = j.fix(i);
+          const bool fix = j.fix(blk);
           uint32_t bar;
           if (fix) {
             mbar_arrive_expect_tx(tail + r.stage, bytes);
@@ -831,11 +936,17 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
           }
           pending[r.stage] = (int)r.phase + (fix ? 2 : 0);
           uint8_t *a = sm + r.stage * C::STAGE, *b = a + AT * TILE;
-          const int row = j.lo + i * BK;
+          const int term = p.passes == 1 ? SPLIT_PASSES - 1 : q;
+          const int row = j.lo + blk * BK;
+          const int ya = term_a(term) * (int)p.rows + row, yb = term_b(term) * (int)p.rows + row;
+          if (++blk == j.kb0) {
+            blk = 0;
+            ++q;
+          }
 #pragma unroll
           for (int c = 0; c < 2 * AT; ++c)
-            load_2d<2>(&tmA, a + c * BOX, bar, n0 + c / 2 * 256 + c % 2 * 64, row, pol);
-          for (int c = 0; c < nbox; ++c) load_2d<2>(&tmB, b + c * BOX, bar, k0 + c * 64, row, pol);
+            load_2d<2>(&tmA, a + c * BOX, bar, n0 + c / 2 * 256 + c % 2 * 64, ya, pol);
+          for (int c = 0; c < nbox; ++c) load_2d<2>(&tmB, b + c * BOX, bar, k0 + c * 64, yb, pol);
           r.next(STAGES);
         }
       }
@@ -850,7 +961,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
         if (j.kb == 0) continue;
         const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
         uint32_t d = 0;
-        for (int i = 0; i < j.kb; ++i) {
+        for (int i = 0, blk = 0; i < j.kb; ++i, blk = blk + 1 == j.kb0 ? 0 : blk + 1) {
           const bool first = i == 0 || (C::SEGS && i % SEG == 0);
           if (first) {
             if (i > 0) {
@@ -864,7 +975,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
           pending[r.stage] = -1;
           tc_fence_after();
           const uint32_t a = smem_u32(sm + r.stage * C::STAGE), b = a + AT * TILE;
-          const int steps = i == j.kb - 1 ? (j.tail + 15) / 16 : BK / 16;
+          const int steps = (j.depth(blk) + 15) / 16;
           for (int s = 0; s < steps; ++s)
 #pragma unroll
             for (int c = 0; c < AT; ++c)
@@ -889,12 +1000,12 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     Ring r;
     for (int64_t tile = unit; tile < total; tile += nunits) {
       const Job j = job(tile);
-      for (int i = 0; i < j.kb; ++i) {
+      for (int i = 0, blk = 0; i < j.kb; ++i, blk = blk + 1 == j.kb0 ? 0 : blk + 1) {
         if (!wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
           tile = total;
           break;
         }
-        if (j.fix(i)) {
+        if (j.fix(blk)) {
           // rows tail .. next multiple of 16 of every 64-column box: 128
           // bytes each, whole rows, so the swizzle does not matter
           uint8_t *st = sm + r.stage * C::STAGE + j.tail * 128;
@@ -945,12 +1056,25 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
         for (int i = 0; i < 8; ++i)
           *reinterpret_cast<uint4 *>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
               make_uint4(word(4 * i), word(4 * i + 1), word(4 * i + 2), word(4 * i + 3));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          store_3d(&tmC, stg, k0, n0, j.g);
-          store_commit();
+        if (p.tma_store) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            store_3d(&tmC, stg, k0, n0, j.g);
+            store_commit();
+          }
+          return;
         }
+        // rows off the 16-byte pitch: a row of the buffer at a time
+        __syncwarp();
+        const int nr = min(32, p.n - n0), nc = min(CH, p.k - k0);
+        TO *o = static_cast<TO *>(p.dw) + ((size_t)j.g * p.n + n0) * p.k + k0;
+        for (int r = 0; r < nr; ++r, o += p.k)
+          for (int c = lane; c < nc; c += 32) {
+            constexpr int V = 16 / sizeof(TO);  // values of a 16-byte unit
+            o[c] = *reinterpret_cast<const TO *>(stg + r * 128 + (((c / V) ^ (r & 7)) << 4) + c % V * sizeof(TO));
+          }
+        __syncwarp();
       };
       auto emit = [&](float (&v)[CH], int c) {
         const int n0 = j.n0 + (int)rank * BM + q * 32, k0 = j.k0 + half * 128 + c * CH;

@@ -85,6 +85,8 @@ struct Product {
   const int32_t *offsets;
   void *out;
   int accumulate;
+  void *ws;
+  size_t ws_bytes;
   int32_t *status;
   cudaStream_t stream;
 };
@@ -195,141 +197,266 @@ int64_t row_tiles(const moe_grouped_shape *s, int bn) {
   return s->rows / bn + (s->rows < s->groups ? s->rows : s->groups);
 }
 
-struct RowMaps {
-  CUtensorMap a0, a1, b0, b1;
+// ------------------------------------------------------------------ staging
+
+// A matrix that a tensor-core product reads: rows x cols, row-major.
+struct Operand {
+  const void *p;
+  int64_t rows;
+  int cols;
 };
 
-// Maps of a product with rows x0 (and x1) [rows, contract] and weights w0
-// (and w1); `kmajor`: weights [G, F, contract], else [G, contract, F].
-template <typename C>
-bool row_maps(RowMaps *m, const moe_grouped_shape *s, const void *w0, const void *w1,
-              const void *x0, const void *x1, uint64_t F, uint64_t contract) {
-  auto wmap = [&](CUtensorMap *t, const void *w) {
-    return C::KMAJOR ? tensor_map(t, w, MOE_BF16, s->groups, F, contract, tcg::BM)
-                     : tensor_map(t, w, MOE_BF16, s->groups, contract, F, 64);
-  };
-  auto xmap = [&](CUtensorMap *t, const void *x) {
-    return tensor_map(t, x, MOE_BF16, 0, s->rows, contract, C::BOXN);
-  };
-  if (!wmap(&m->a0, w0) || !xmap(&m->b0, x0)) return false;
-  m->a1 = m->a0;
-  m->b1 = m->b0;
-  return (!w1 || wmap(&m->a1, w1)) && (!x1 || xmap(&m->b1, x1));
+int padded(int cols) { return (cols + 7) / 8 * 8; }
+
+// How a product runs.  direct: TMA reads the operands as they are.  staged:
+// through bf16 copies in the workspace (see stage_rows).  Otherwise on the
+// CUDA cores.
+struct Plan {
+  bool direct = false, staged = false;
+  int terms = 1;         // planes of a staged operand
+  size_t bytes = 0;      // of the staged operands
+  bool tensor() const { return direct || staged; }
+};
+
+// Operands of a product with `flops` operations.  aligned: every operand is
+// 16-byte aligned (their addresses are not looked at).
+Plan plan(const Operand *ops, int n, moe_dtype dt, double flops, bool aligned) {
+  Plan p;
+  p.terms = dt == MOE_F32 ? tcg::SPLIT_TERMS : 1;
+  bool fits = dt == MOE_BF16;
+  for (int i = 0; i < n; ++i) {
+    fits = fits && aligned && ops[i].cols % 8 == 0;
+    if (ops[i].rows * p.terms >= ((int64_t)1 << 31)) return p;  // 32-bit row coordinates
+    p.bytes += align_up((size_t)ops[i].rows * padded(ops[i].cols) * p.terms * 2, 256);
+  }
+  if (fits) {
+    p.direct = true;
+    p.bytes = 0;
+    return p;
+  }
+  // Below this the copies and their launches cost more than the CUDA cores'
+  // lower rate (measured: see the table of XXX)
+  constexpr double WORTH = 1e8;
+  p.staged = flops >= WORTH;
+  if (!p.staged) p.bytes = 0;
+  return p;
 }
 
+bool all_aligned(const Operand *ops, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!aligned(ops[i].p, 16)) return false;
+  return true;
+}
+
+// Copies every operand into the workspace and points it there.
+moe_status stage(Operand *ops, int n, moe_dtype dt, void *ws, cudaStream_t s) {
+  uint8_t *at = static_cast<uint8_t *>(ws);
+  const int nsm = sm_count();
+  if (nsm < 1) return MOE_ERR_CUDA;
+  for (int i = 0; i < n; ++i) {
+    const int kp = padded(ops[i].cols);
+    const int64_t blocks = (ops[i].rows * (kp / 8) + 255) / 256, most = (int64_t)nsm * 8;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    bf16 *dst = reinterpret_cast<bf16 *>(at);
+    if (dt == MOE_F32)
+      tcg::stage_rows<float, tcg::SPLIT_TERMS><<<grid, 256, 0, s>>>(static_cast<const float *>(ops[i].p), ops[i].rows, ops[i].cols, kp, dst);
+    else
+      tcg::stage_rows<bf16, 1><<<grid, 256, 0, s>>>(static_cast<const bf16 *>(ops[i].p), ops[i].rows, ops[i].cols, kp, dst);
+    const moe_status st = launch_status();
+    if (st != MOE_OK) return st;
+    at += align_up((size_t)ops[i].rows * kp * (dt == MOE_F32 ? tcg::SPLIT_TERMS : 1) * 2, 256);
+    ops[i].p = dst;
+    ops[i].cols = kp;
+  }
+  return MOE_OK;
+}
+
+// --------------------------------------------------------- tensor-core launches
+
+// A product with one result row per input row: F features, contracting over
+// `contract` values; x and w as planned (w1, x1: a second weight or source).
+struct RowJob {
+  const moe_grouped_shape *s;
+  int F, contract, terms;
+  Operand x0, w0, x1, w1;  // w1, x1: p NULL if there is none
+  tcg::RowParams p;
+  cudaStream_t stream;
+};
+
 template <int OP, int CG, int AT, int BN, int STAGES, bool SEGS, typename TO>
-moe_status launch_rows(const moe_grouped_shape *s, const void *w0, const void *w1, const void *x0,
-                       const void *x1, int F, int contract, tcg::RowParams p, cudaStream_t st) {
+moe_status launch_rows(const RowJob &j) {
   using C = tcg::RowCfg<OP, CG, AT, BN, STAGES, SEGS>;
-  RowMaps m;
-  if (!row_maps<C>(&m, s, w0, w1, x0, x1, F, contract)) return MOE_ERR_CUDA;
+  const moe_grouped_shape *s = j.s;
+  const uint64_t planes = (uint64_t)j.terms * s->groups, wrows = C::KMAJOR ? j.F : j.contract;
+  auto wmap = [&](CUtensorMap *t, const Operand &w) {
+    return tensor_map(t, w.p, MOE_BF16, planes, wrows, w.cols, C::KMAJOR ? tcg::BM : 64);
+  };
+  auto xmap = [&](CUtensorMap *t, const Operand &x) {
+    return tensor_map(t, x.p, MOE_BF16, 0, (uint64_t)j.terms * s->rows, x.cols, C::BOXN);
+  };
+  CUtensorMap a0, a1, b0, b1;
+  if (!wmap(&a0, j.w0) || !xmap(&b0, j.x0)) return MOE_ERR_CUDA;
+  a1 = a0;
+  b1 = b0;
+  if ((j.w1.p && !wmap(&a1, j.w1)) || (j.x1.p && !xmap(&b1, j.x1))) return MOE_ERR_CUDA;
+  tcg::RowParams p = j.p;
   p.G = s->groups;
-  p.F = F;
+  p.F = j.F;
   p.rows = s->rows;
-  p.kb0 = (contract + tcg::BK - 1) / tcg::BK;
-  p.kb = x1 ? 2 * p.kb0 : p.kb0;
-  const int64_t tiles = row_tiles(s, BN) * ((F + C::FEAT - 1) / C::FEAT);
-  return launch_persistent<tcg::rows_gemm<OP, CG, AT, BN, STAGES, SEGS, TO>>(C::NT, C::smem(p.G), CG, tiles,
-                           st, m.a0, m.a1, m.b0, m.b1, (const tcg::RowParams)p);
+  p.passes = j.terms == 1 ? 1 : tcg::SPLIT_PASSES;
+  p.kb0 = (j.contract + tcg::BK - 1) / tcg::BK;
+  p.kb = p.kb0 * p.passes * (j.x1.p ? 2 : 1);
+  const int64_t tiles = row_tiles(s, BN) * ((j.F + C::FEAT - 1) / C::FEAT);
+  return launch_persistent<tcg::rows_gemm<OP, CG, AT, BN, STAGES, SEGS, TO>>(
+      C::NT, C::smem(p.G), CG, tiles, j.stream, a0, a1, b0, b1, (const tcg::RowParams)p);
 }
 
 // rows of a group on average
 int64_t mean_rows(const moe_grouped_shape *s) { return (s->rows + s->groups - 1) / s->groups; }
 
 template <int OP, typename TO>
-moe_status tc_rows(const Product &p, int F, int contract) {
-  tcg::RowParams r = {};
-  r.offsets = p.offsets;
-  r.out = p.out;
-  r.status = p.status;
-  const auto *s = p.s;
-  auto run = [&](auto launch) { return launch(s, p.b0, p.b1, p.a0, p.a1, F, contract, r, p.stream); };
+moe_status tc_rows(const RowJob &j) {
   if constexpr (sizeof(TO) == 4) {  // fp32 results: sums in segments
-    if (mean_rows(s) <= 48 || F < 256) return run(launch_rows<OP, 1, 1, 64, 8, true, TO>);
-    return run(launch_rows<OP, 2, 1, 256, 6, true, TO>);
+    if (mean_rows(j.s) <= 48 || j.F < 256) return launch_rows<OP, 1, 1, 64, 8, true, TO>(j);
+    return launch_rows<OP, 2, 1, 256, 6, true, TO>(j);
   } else {
-    if (mean_rows(s) <= 48) return run(launch_rows<OP, 1, 1, 64, 8, false, TO>);
-    if (F < 512) return run(launch_rows<OP, 1, 1, 256, 4, false, TO>);
-    return run(launch_rows<OP, 2, 2, 256, 4, false, TO>);
+    if (mean_rows(j.s) <= 48) return launch_rows<OP, 1, 1, 64, 8, false, TO>(j);
+    if (j.F < 512) return launch_rows<OP, 1, 1, 256, 4, false, TO>(j);
+    return launch_rows<OP, 2, 2, 256, 4, false, TO>(j);
   }
 }
 
-int scale_blocks(int n) { return (n + ckpt::BLOCK - 1) / ckpt::BLOCK; }
-
-// Sizes the tensor-core kernels take: rows of 16 bytes, and 4 hidden features
-// written at a time.
-bool tc_up_sizes(const moe_grouped_shape *s, moe_dtype dt) {
-  return dt == MOE_BF16 && s->k % 8 == 0 && s->n % 4 == 0;
-}
-bool tc_bwd_sizes(const moe_grouped_shape *s, moe_dtype dt) {
-  return dt == MOE_BF16 && s->k % 8 == 0 && s->n % 8 == 0;
+// The first matmul with its checkpoint, and the gradients of the hidden rows.
+template <typename TO>
+moe_status tc_up(const RowJob &j) {
+  if (mean_rows(j.s) <= 48 || j.F < 256) return launch_rows<tcg::UP, 1, 2, 64, 5, true, TO>(j);
+  return launch_rows<tcg::UP, 2, 2, 128, 5, true, TO>(j);
 }
 
-// The first matmul with its checkpoint (n hidden features from k), and the
-// gradients of the hidden rows (contracting over k).
-moe_status tc_up(const moe_grouped_shape *s, const void *x, const void *w1, const void *w3,
-                 const tcg::RowParams &r, cudaStream_t st) {
-  if (mean_rows(s) <= 48 || s->n < 256)
-    return launch_rows<tcg::UP, 1, 2, 64, 5, true, bf16>(s, w1, w3, x, nullptr, s->n, s->k, r, st);
-  return launch_rows<tcg::UP, 2, 2, 128, 5, true, bf16>(s, w1, w3, x, nullptr, s->n, s->k, r, st);
-}
-
-moe_status tc_bwd(const moe_grouped_shape *s, const void *dy, const void *w2,
-                  const tcg::RowParams &r, cudaStream_t st) {
-  if (mean_rows(s) <= 48 || s->n < 256)
-    return launch_rows<tcg::BWD, 1, 1, 64, 8, true, bf16>(s, w2, nullptr, dy, nullptr, s->n, s->k, r, st);
-  return launch_rows<tcg::BWD, 2, 1, 256, 6, true, bf16>(s, w2, nullptr, dy, nullptr, s->n, s->k, r, st);
+template <typename TO>
+moe_status tc_bwd(const RowJob &j) {
+  if (mean_rows(j.s) <= 48 || j.F < 256) return launch_rows<tcg::BWD, 1, 1, 64, 8, true, TO>(j);
+  return launch_rows<tcg::BWD, 2, 1, 256, 6, true, TO>(j);
 }
 
 template <typename TO, int AT>
-moe_status launch_dw(const Product &p) {
+moe_status launch_dw(const Product &p, const Operand *ops, int terms) {
   using C = tcg::DwCfg<TO, AT>;
   const auto *s = p.s;
+  const uint64_t rows = (uint64_t)terms * s->rows;
+  const bool store = aligned(p.out, 16) && (int64_t)s->k * sizeof(TO) % 16 == 0;
   CUtensorMap a, b, c;
-  if (!tensor_map(&a, p.a0, MOE_BF16, 0, s->rows, s->n, tcg::BK) ||
-      !tensor_map(&b, p.b0, MOE_BF16, 0, s->rows, s->k, tcg::BK) ||
-      !tensor_map(&c, p.out, p.out_dt, s->groups, s->n, s->k, 32))
+  if (!tensor_map(&a, ops[0].p, MOE_BF16, 0, rows, ops[0].cols, tcg::BK) ||
+      !tensor_map(&b, ops[1].p, MOE_BF16, 0, rows, ops[1].cols, tcg::BK))
     return MOE_ERR_CUDA;
-  const tcg::DwParams d{p.offsets, s->groups, s->n, s->k, s->rows, p.out, p.accumulate, p.status};
+  c = a;
+  if (store && !tensor_map(&c, p.out, p.out_dt, s->groups, s->n, s->k, 32)) return MOE_ERR_CUDA;
+  const tcg::DwParams d{p.offsets, s->groups, s->n, s->k, s->rows, p.out, p.accumulate,
+                        terms == 1 ? 1 : tcg::SPLIT_PASSES, store, p.status};
   const int64_t tiles = (int64_t)s->groups * ((s->n + C::FEAT - 1) / C::FEAT) * ((s->k + 255) / 256);
   return launch_persistent<tcg::dw_gemm<TO, AT>>(C::NT, (size_t)C::BYTES, 2, tiles, p.stream, a, b, c, d);
 }
 
-moe_status tc_dw(const Product &p) {
-  if (p.out_dt == MOE_F32) return launch_dw<float, 1>(p);
+moe_status tc_dw(const Product &p, const Operand *ops, int terms) {
+  if (p.out_dt == MOE_F32) return launch_dw<float, 1>(p, ops, terms);
   // a bf16 sum with what is there already adds in fp32, which the packed
   // results of the wider tile no longer are
-  if (p.accumulate || p.s->n <= 256) return launch_dw<bf16, 1>(p);
-  return launch_dw<bf16, 2>(p);
+  if (p.accumulate || p.s->n <= 256) return launch_dw<bf16, 1>(p, ops, terms);
+  return launch_dw<bf16, 2>(p, ops, terms);
 }
 
-// Tensor maps need 16-byte aligned addresses and row pitches.
-bool tc_operand(const void *p, int64_t cols, moe_dtype dt) {
-  return aligned(p, 16) && cols * elem(dt) % 16 == 0;
+// ---------------------------------------------------- operands of the products
+
+double flops_of(const moe_grouped_shape *s, int products) {
+  return 2.0 * products * (double)s->rows * s->n * s->k;
+}
+
+int linear_ops(const moe_grouped_shape *s, const void *x, const void *w, Operand *o) {
+  o[0] = {x, s->rows, s->k};
+  o[1] = {w, (int64_t)s->groups * s->n, s->k};
+  return 2;
+}
+int dx_ops(const moe_grouped_shape *s, const void *dy, const void *w, const void *dy2, const void *w2,
+           bool two, Operand *o) {
+  o[0] = {dy, s->rows, s->n};
+  o[1] = {w, (int64_t)s->groups * s->n, s->k};
+  o[2] = {dy2, s->rows, s->n};
+  o[3] = {w2, (int64_t)s->groups * s->n, s->k};
+  return two ? 4 : 2;
+}
+int dw_ops(const moe_grouped_shape *s, const void *dy, const void *x, Operand *o) {
+  o[0] = {dy, s->rows, s->n};
+  o[1] = {x, s->rows, s->k};
+  return 2;
+}
+int up_ops(const moe_grouped_shape *s, const void *x, const void *w1, const void *w3, Operand *o) {
+  o[0] = {x, s->rows, s->k};
+  o[1] = {w1, (int64_t)s->groups * s->n, s->k};
+  o[2] = {w3, (int64_t)s->groups * s->n, s->k};
+  return 3;
+}
+int bwd_ops(const moe_grouped_shape *s, const void *dy, const void *w2, Operand *o) {
+  o[0] = {dy, s->rows, s->k};
+  o[1] = {w2, (int64_t)s->groups * s->k, s->n};
+  return 2;
+}
+
+// The plan for operands whose addresses are known; a staged one needs its
+// workspace (without it the CUDA cores do).
+Plan plan_call(const Operand *o, int n, moe_dtype dt, double flops, const void *ws, size_t ws_bytes) {
+  Plan p = plan(o, n, dt, flops, all_aligned(o, n));
+  if (p.staged && (!ws || !aligned(ws, 16) || ws_bytes < p.bytes)) p.staged = false;
+  return p;
 }
 
 moe_status run_linear(const Product &p) {
-  if (p.dt == MOE_BF16 && tc_operand(p.a0, p.s->k, p.dt) && tc_operand(p.b0, p.s->k, p.dt))
-    return p.out_dt == MOE_F32 ? tc_rows<tcg::LIN, float>(p, p.s->n, p.s->k)
-                               : tc_rows<tcg::LIN, bf16>(p, p.s->n, p.s->k);
-  return simt_product<simt::LIN>(simt_args(p), p.dt, p.out_dt, p.stream);
+  Operand o[4];
+  const int n = linear_ops(p.s, p.a0, p.b0, o);
+  const Plan pl = plan_call(o, n, p.dt, flops_of(p.s, 1), p.ws, p.ws_bytes);
+  if (!pl.tensor()) return simt_product<simt::LIN>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (pl.staged) {
+    const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
+    if (st != MOE_OK) return st;
+  }
+  RowJob j{p.s, p.s->n, p.s->k, pl.terms, o[0], o[1], {}, {}, {}, p.stream};
+  j.p.offsets = p.offsets;
+  j.p.out = p.out;
+  j.p.status = p.status;
+  return p.out_dt == MOE_F32 ? tc_rows<tcg::LIN, float>(j) : tc_rows<tcg::LIN, bf16>(j);
 }
 
 moe_status run_dx(const Product &p) {
-  if (p.dt == MOE_BF16 && tc_operand(p.a0, p.s->n, p.dt) && tc_operand(p.b0, p.s->k, p.dt) &&
-      tc_operand(p.a1, p.s->n, p.dt) && tc_operand(p.b1, p.s->k, p.dt))
-    return p.out_dt == MOE_F32 ? tc_rows<tcg::DX, float>(p, p.s->k, p.s->n)
-                               : tc_rows<tcg::DX, bf16>(p, p.s->k, p.s->n);
-  return simt_product<simt::DX>(simt_args(p), p.dt, p.out_dt, p.stream);
+  Operand o[4];
+  const bool two = p.a1 != nullptr;
+  const int n = dx_ops(p.s, p.a0, p.b0, p.a1, p.b1, two, o);
+  const Plan pl = plan_call(o, n, p.dt, flops_of(p.s, two ? 2 : 1), p.ws, p.ws_bytes);
+  if (!pl.tensor()) return simt_product<simt::DX>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (pl.staged) {
+    const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
+    if (st != MOE_OK) return st;
+  }
+  RowJob j{p.s, p.s->k, p.s->n, pl.terms, o[0], o[1], o[2], o[3], {}, p.stream};
+  j.p.offsets = p.offsets;
+  j.p.out = p.out;
+  j.p.status = p.status;
+  return p.out_dt == MOE_F32 ? tc_rows<tcg::DX, float>(j) : tc_rows<tcg::DX, bf16>(j);
 }
 
 moe_status run_dw(const Product &p) {
+  Operand o[4];
+  const int n = dw_ops(p.s, p.a0, p.b0, o);
+  const Plan pl = plan_call(o, n, p.dt, flops_of(p.s, 1), p.ws, p.ws_bytes);
   // without rows there is nothing to map; the CUDA-core kernel writes the zeros
-  if (p.dt == MOE_BF16 && p.s->rows > 0 && tc_operand(p.a0, p.s->n, p.dt) &&
-      tc_operand(p.b0, p.s->k, p.dt) && tc_operand(p.out, p.s->k, p.out_dt))
-    return tc_dw(p);
-  return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (!pl.tensor() || p.s->rows == 0)
+    return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (pl.staged) {
+    const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
+    if (st != MOE_OK) return st;
+  }
+  return tc_dw(p, o, pl.terms);
 }
+
+int scale_blocks(int n) { return (n + ckpt::BLOCK - 1) / ckpt::BLOCK; }
 
 unsigned row_grid(int64_t warps) {
   const int64_t blocks = (warps + ckpt::ROW_THREADS / 32 - 1) / (ckpt::ROW_THREADS / 32);
@@ -342,45 +469,68 @@ unsigned row_grid(int64_t warps) {
 
 using namespace moe;
 
+MOE_EXPORT size_t moe_grouped_linear_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                                    int32_t aligned) {
+  if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
+  Operand o[4];
+  return plan(o, linear_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned).bytes;
+}
+
+MOE_EXPORT size_t moe_grouped_linear_dx_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                                       int32_t two, int32_t aligned) {
+  if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
+  Operand o[4];
+  const int n = dx_ops(s, nullptr, nullptr, nullptr, nullptr, two != 0, o);
+  return plan(o, n, dt, flops_of(s, two ? 2 : 1), aligned).bytes;
+}
+
+MOE_EXPORT size_t moe_grouped_linear_dw_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
+                                                       int32_t aligned) {
+  if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
+  Operand o[4];
+  return plan(o, dw_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned).bytes;
+}
+
 MOE_EXPORT moe_status moe_grouped_linear(const moe_grouped_shape *s, const void *x, moe_dtype dt,
                                          const void *w, const int32_t *offsets, void *y,
-                                         moe_dtype y_dt, int32_t *dev_status,
-                                         moe_stream_t stream) {
+                                         moe_dtype y_dt, void *ws, size_t ws_bytes,
+                                         int32_t *dev_status, moe_stream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
   if (!act_type(dt) || !act_type(y_dt)) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0) return MOE_OK;
   if (!x || !w || !offsets || !y) return MOE_ERR_INVALID;
-  return run_linear({s, dt, y_dt, x, w, nullptr, nullptr, offsets, y, 0, dev_status,
+  return run_linear({s, dt, y_dt, x, w, nullptr, nullptr, offsets, y, 0, ws, ws_bytes, dev_status,
                      as_stream(stream)});
 }
 
 MOE_EXPORT moe_status moe_grouped_linear_dx(const moe_grouped_shape *s, const void *dy,
                                             moe_dtype dt, const void *w, const void *dy2,
                                             const void *w2, const int32_t *offsets, void *dx,
-                                            moe_dtype dx_dt, int32_t *dev_status,
-                                            moe_stream_t stream) {
+                                            moe_dtype dx_dt, void *ws, size_t ws_bytes,
+                                            int32_t *dev_status, moe_stream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
   if (!act_type(dt) || !act_type(dx_dt)) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0) return MOE_OK;  // (an empty dy2 may well be NULL)
   if ((dy2 == nullptr) != (w2 == nullptr)) return MOE_ERR_INVALID;
   if (!dy || !w || !offsets || !dx) return MOE_ERR_INVALID;
-  return run_dx({s, dt, dx_dt, dy, w, dy2, w2, offsets, dx, 0, dev_status, as_stream(stream)});
+  return run_dx({s, dt, dx_dt, dy, w, dy2, w2, offsets, dx, 0, ws, ws_bytes, dev_status, as_stream(stream)});
 }
 
 MOE_EXPORT moe_status moe_grouped_linear_dw(const moe_grouped_shape *s, const void *dy,
                                             moe_dtype dt, const void *x, const int32_t *offsets,
-                                            void *dw, moe_dtype dw_dt, int32_t accumulate,
-                                            int32_t *dev_status, moe_stream_t stream) {
+                                            void *dw, moe_dtype dw_dt, int32_t accumulate, void *ws,
+                                            size_t ws_bytes, int32_t *dev_status,
+                                            moe_stream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
   if (!act_type(dt) || !act_type(dw_dt)) return MOE_ERR_UNSUPPORTED;
   if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID;
   // without rows the row buffers may be empty (NULL), but dw is still written
   if (!offsets || !dw || (s->rows > 0 && (!dy || !x))) return MOE_ERR_INVALID;
-  return run_dw({s, dt, dw_dt, dy, x, nullptr, nullptr, offsets, dw, accumulate, dev_status,
-                 as_stream(stream)});
+  return run_dw({s, dt, dw_dt, dy, x, nullptr, nullptr, offsets, dw, accumulate, ws, ws_bytes,
+                 dev_status, as_stream(stream)});
 }
 
 MOE_EXPORT moe_status moe_checkpoint_rows(const void *src, moe_dtype dt, int64_t rows, int32_t k,
@@ -440,8 +590,10 @@ MOE_EXPORT moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps
 MOE_EXPORT size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
                                                        int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
-  if (aligned && tc_up_sizes(s, dt)) return 0;
-  return 2 * align_up((size_t)s->rows * s->n * 4, 256);  // the two projections in fp32
+  Operand o[4];
+  const Plan p = plan(o, up_ops(s, nullptr, nullptr, nullptr, o), dt, flops_of(s, 2), aligned);
+  // on the CUDA cores: the two projections in fp32
+  return p.tensor() ? p.bytes : 2 * align_up((size_t)s->rows * s->n * 4, 256);
 }
 
 MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const void *x,
@@ -458,23 +610,27 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
     return MOE_ERR_INVALID;
   cudaStream_t cs = as_stream(stream);
   const ckpt::Saved sv{codes_a, exps_a, codes_u, exps_u};
-  const bool tc = tc_up_sizes(s, dt) && aligned(x, 16) && aligned(w1, 16) && aligned(w3, 16) &&
-                  aligned(h, 8) && aligned(codes_a, 4) && aligned(codes_u, 4);
-  const size_t need = moe_swiglu_checkpoint_workspace_size(s, dt, tc);
-  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
-  if (tc) {
-    tcg::RowParams r = {};
-    r.offsets = offsets;
-    r.out = h;
-    r.status = dev_status;
-    r.saved = sv;
-    return tc_up(s, x, w1, w3, r, cs);
+  Operand o[4];
+  const int n = up_ops(s, x, w1, w3, o);
+  const bool fits = all_aligned(o, n);
+  const Plan p = plan(o, n, dt, flops_of(s, 2), fits);
+  const size_t need = moe_swiglu_checkpoint_workspace_size(s, dt, fits);
+  if (need && (!ws || !aligned(ws, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (p.tensor()) {
+    if (p.staged && (st = stage(o, n, dt, ws, cs)) != MOE_OK) return st;
+    RowJob j{s, s->n, s->k, p.terms, o[0], o[1], {}, o[2], {}, cs};
+    j.p.offsets = offsets;
+    j.p.out = h;
+    j.p.status = dev_status;
+    j.p.saved = sv;
+    j.p.vec = s->n % 4 == 0 && aligned(h, 4 * elem(dt)) && aligned(codes_a, 4) && aligned(codes_u, 4);
+    return dt == MOE_F32 ? tc_up<float>(j) : tc_up<bf16>(j);
   }
   float *a = static_cast<float *>(ws);
   float *u = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + align_up((size_t)s->rows * s->n * 4, 256));
-  if ((st = run_linear({s, dt, MOE_F32, x, w1, nullptr, nullptr, offsets, a, 0, dev_status, cs})) != MOE_OK)
+  if ((st = run_linear({s, dt, MOE_F32, x, w1, nullptr, nullptr, offsets, a, 0, nullptr, 0, dev_status, cs})) != MOE_OK)
     return st;
-  if ((st = run_linear({s, dt, MOE_F32, x, w3, nullptr, nullptr, offsets, u, 0, dev_status, cs})) != MOE_OK)
+  if ((st = run_linear({s, dt, MOE_F32, x, w3, nullptr, nullptr, offsets, u, 0, nullptr, 0, dev_status, cs})) != MOE_OK)
     return st;
   const unsigned grid = row_grid(s->rows * scale_blocks(s->n));
   if (dt == MOE_F32)
@@ -484,12 +640,17 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
   return launch_status();
 }
 
+// one term of dgate for 32 hidden features
+static size_t part_bytes(const moe_grouped_shape *s) {
+  return align_up((size_t)s->rows * scale_blocks(s->n) * 4, 256);
+}
+
 MOE_EXPORT size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
                                                      int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
-  // one term of dgate for 32 hidden features, or dh in fp32
-  if (aligned && tc_bwd_sizes(s, dt)) return (size_t)s->rows * scale_blocks(s->n) * 4;
-  return (size_t)s->rows * s->n * 4;
+  Operand o[4];
+  const Plan p = plan(o, bwd_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned);
+  return p.tensor() ? part_bytes(s) + p.bytes : (size_t)s->rows * s->n * 4;  // else dh in fp32
 }
 
 MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
@@ -509,28 +670,36 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
   cudaStream_t cs = as_stream(stream);
   const ckpt::Saved sv{const_cast<uint8_t *>(codes_a), const_cast<uint8_t *>(exps_a),
                        const_cast<uint8_t *>(codes_u), const_cast<uint8_t *>(exps_u)};
-  const bool tc = tc_bwd_sizes(s, dt) && aligned(dy, 16) && aligned(w2, 16) && aligned(codes_a, 4) &&
-                  aligned(codes_u, 4) && aligned(da, 8) && aligned(du, 8) && aligned(hg, 8);
-  if (!ws || ws_bytes < moe_swiglu_backward_workspace_size(s, dt, tc)) return MOE_ERR_WORKSPACE;
-  if (tc) {
-    tcg::RowParams r = {};
-    r.offsets = offsets;
-    r.status = dev_status;
-    r.saved = sv;
-    r.gate = gate;
-    r.da = static_cast<bf16 *>(da);
-    r.du = static_cast<bf16 *>(du);
-    r.hg = static_cast<bf16 *>(hg);
-    r.part = static_cast<float *>(ws);
-    if ((st = tc_bwd(s, dy, w2, r, cs)) != MOE_OK) return st;
+  Operand o[4];
+  const int n = bwd_ops(s, dy, w2, o);
+  const bool fits = all_aligned(o, n);
+  const Plan p = plan(o, n, dt, flops_of(s, 1), fits);
+  if (!ws || !aligned(ws, 16) || ws_bytes < moe_swiglu_backward_workspace_size(s, dt, fits))
+    return MOE_ERR_WORKSPACE;
+  if (p.tensor()) {
+    if (p.staged && (st = stage(o, n, dt, static_cast<uint8_t *>(ws) + part_bytes(s), cs)) != MOE_OK)
+      return st;
+    RowJob j{s, s->n, s->k, p.terms, o[0], o[1], {}, {}, {}, cs};
+    j.p.offsets = offsets;
+    j.p.status = dev_status;
+    j.p.saved = sv;
+    j.p.gate = gate;
+    j.p.da = da;
+    j.p.du = du;
+    j.p.hg = hg;
+    j.p.part = static_cast<float *>(ws);
+    const size_t v = 4 * elem(dt);
+    j.p.vec = s->n % 4 == 0 && aligned(codes_a, 4) && aligned(codes_u, 4) && aligned(da, v) &&
+              aligned(du, v) && aligned(hg, v);
+    if ((st = dt == MOE_F32 ? tc_bwd<float>(j) : tc_bwd<bf16>(j)) != MOE_OK) return st;
     tcg::sum_parts<<<(unsigned)((s->rows + 255) / 256), 256, 0, cs>>>(
-        r.part, offsets, s->groups, s->rows, scale_blocks(s->n), dgate);
+        j.p.part, offsets, s->groups, s->rows, scale_blocks(s->n), dgate);
     return launch_status();
   }
   float *dh = static_cast<float *>(ws);
   // dh = dy w2: the input gradient of a linear layer from n features to k
   const moe_grouped_shape lin{s->groups, s->k, s->n, s->rows};
-  if ((st = run_dx({&lin, dt, MOE_F32, dy, w2, nullptr, nullptr, offsets, dh, 0, dev_status, cs})) != MOE_OK)
+  if ((st = run_dx({&lin, dt, MOE_F32, dy, w2, nullptr, nullptr, offsets, dh, 0, nullptr, 0, dev_status, cs})) != MOE_OK)
     return st;
   const unsigned grid = row_grid(s->rows * (ckpt::ROW_THREADS / 32));
   if (dt == MOE_F32)

@@ -115,6 +115,16 @@ def _status(status: Optional[torch.Tensor]) -> Optional[int]:
     return _ptr(status)
 
 
+def _workspace(sym: str, shape: MoEGroupedShape, dt: int, dev, operands, *flags: int):
+    """(tensor or None, address or None, bytes) of the workspace `sym` asks for."""
+    aligned = not any(t.data_ptr() % 16 for t in operands)
+    need = _entry(sym)(ctypes.byref(shape), dt, *flags, int(aligned))
+    if not need:
+        return None, None, 0
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    return ws, ws.data_ptr(), need
+
+
 def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
                    out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
                    status: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -127,9 +137,10 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
     dt = _dtype(x, w)
     rows, n = x.shape[0], w.shape[1]
     out = _out(out, (rows, n), out_dtype or (x.dtype if out is None else out.dtype), dev)
-    _call(dev, "moe_grouped_linear", ctypes.byref(MoEGroupedShape(G, n, x.shape[1], rows)),
-          x.data_ptr(), dt, w.data_ptr(), offsets.data_ptr(), out.data_ptr(), _DT[out.dtype],
-          _status(status))
+    shape = MoEGroupedShape(G, n, x.shape[1], rows)
+    ws, at, nws = _workspace("moe_grouped_linear_workspace_size", shape, dt, dev, (x, w))
+    _call(dev, "moe_grouped_linear", ctypes.byref(shape), x.data_ptr(), dt, w.data_ptr(),
+          offsets.data_ptr(), out.data_ptr(), _DT[out.dtype], at, nws, _status(status))
     return out
 
 
@@ -150,9 +161,13 @@ def grouped_linear_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, 
         _dtype(dy, dy2, w2)
     rows, k = dy.shape[0], w.shape[2]
     out = _out(out, (rows, k), out_dtype or (dy.dtype if out is None else out.dtype), dev)
-    _call(dev, "moe_grouped_linear_dx", ctypes.byref(MoEGroupedShape(G, w.shape[1], k, rows)),
-          dy.data_ptr(), dt, w.data_ptr(), _ptr(dy2), _ptr(w2), offsets.data_ptr(),
-          out.data_ptr(), _DT[out.dtype], _status(status))
+    shape = MoEGroupedShape(G, w.shape[1], k, rows)
+    two = dy2 is not None
+    ws, at, nws = _workspace("moe_grouped_linear_dx_workspace_size", shape, dt, dev,
+                             (dy, w, dy2, w2) if two else (dy, w), int(two))
+    _call(dev, "moe_grouped_linear_dx", ctypes.byref(shape), dy.data_ptr(), dt, w.data_ptr(),
+          _ptr(dy2), _ptr(w2), offsets.data_ptr(), out.data_ptr(), _DT[out.dtype], at, nws,
+          _status(status))
     return out
 
 
@@ -171,9 +186,11 @@ def grouped_linear_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
     dt = _dtype(dy, x)
     (rows, n), k = dy.shape, x.shape[1]
     out = _out(out, (G, n, k), out_dtype or (dy.dtype if out is None else out.dtype), dev)
-    _call(dev, "moe_grouped_linear_dw", ctypes.byref(MoEGroupedShape(G, n, k, rows)),
-          dy.data_ptr(), dt, x.data_ptr(), offsets.data_ptr(), out.data_ptr(), _DT[out.dtype],
-          int(accumulate), _status(status))
+    shape = MoEGroupedShape(G, n, k, rows)
+    ws, at, nws = _workspace("moe_grouped_linear_dw_workspace_size", shape, dt, dev, (dy, x))
+    _call(dev, "moe_grouped_linear_dw", ctypes.byref(shape), dy.data_ptr(), dt, x.data_ptr(),
+          offsets.data_ptr(), out.data_ptr(), _DT[out.dtype], int(accumulate), at, nws,
+          _status(status))
     return out
 
 
@@ -222,13 +239,6 @@ def restore_rows(ckpt: Checkpoint, index: Optional[torch.Tensor] = None, *,
     return out
 
 
-def _workspace(sym: str, shape: MoEGroupedShape, dt: int, dev, *operands: torch.Tensor):
-    """Device workspace of a swiglu call (None if it needs none)."""
-    aligned = not any(t.data_ptr() % 16 for t in operands)
-    need = _entry(sym)(ctypes.byref(shape), dt, int(aligned))
-    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-
-
 def swiglu_checkpoint(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, offsets: torch.Tensor, *,
                       status: Optional[torch.Tensor] = None):
     """moe_swiglu_checkpoint: (h, a, u) with h = silu(x w1^T) * (x w3^T) by group
@@ -243,12 +253,10 @@ def swiglu_checkpoint(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, offse
     h = torch.empty(rows, n, dtype=x.dtype, device=dev)
     a, u = _empty_ckpt(rows, n, dev), _empty_ckpt(rows, n, dev)
     shape = MoEGroupedShape(G, n, x.shape[1], rows)
-    ws = _workspace("moe_swiglu_checkpoint_workspace_size", shape, dt, dev, x, w1, w3, h, a.codes,
-                    u.codes)
+    ws, at, nws = _workspace("moe_swiglu_checkpoint_workspace_size", shape, dt, dev, (x, w1, w3))
     _call(dev, "moe_swiglu_checkpoint", ctypes.byref(shape), x.data_ptr(), dt, w1.data_ptr(),
           w3.data_ptr(), offsets.data_ptr(), h.data_ptr(), a.codes.data_ptr(), a.exps.data_ptr(),
-          u.codes.data_ptr(), u.exps.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
-          _status(status))
+          u.codes.data_ptr(), u.exps.data_ptr(), at, nws, _status(status))
     return h, a, u
 
 
@@ -271,12 +279,11 @@ def swiglu_backward(dy: torch.Tensor, w2: torch.Tensor, a: Checkpoint, u: Checkp
     da, du, hg = (torch.empty(rows, n, dtype=dy.dtype, device=dev) for _ in range(3))
     dgate = torch.empty(rows, dtype=torch.float32, device=dev)
     shape = MoEGroupedShape(G, n, k, rows)
-    ws = _workspace("moe_swiglu_backward_workspace_size", shape, dt, dev, dy, w2, a.codes, u.codes,
-                    da, du, hg)
+    ws, at, nws = _workspace("moe_swiglu_backward_workspace_size", shape, dt, dev, (dy, w2))
     _call(dev, "moe_swiglu_backward", ctypes.byref(shape), dy.data_ptr(), dt, w2.data_ptr(),
           a.codes.data_ptr(), a.exps.data_ptr(), u.codes.data_ptr(), u.exps.data_ptr(), _ptr(gate),
           offsets.data_ptr(), da.data_ptr(), du.data_ptr(), hg.data_ptr(), dgate.data_ptr(),
-          _ptr(ws), 0 if ws is None else ws.numel(), _status(status))
+          at, nws, _status(status))
     return da, du, hg, dgate
 
 

@@ -20,6 +20,9 @@ SHAPES = [
     ([5, 40, 2], 33, 77),
     ([1, 2], 1, 1),
     ([700], 640, 576),
+    # large enough for the tensor cores although off their alignment
+    ([300, 0, 513, 1, 17], 333, 301),
+    ([21, 33, 90, 40, 64, 15, 77, 8, 130, 1], 607, 449),
 ]
 
 

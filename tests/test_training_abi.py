@@ -45,15 +45,16 @@ BAD_SHAPES = [(dict(groups=0), INVALID), (dict(n=0), INVALID), (dict(k=-1), INVA
 
 
 def linear(s, x=P, dt=BF16, w=P, off=P, y=P, ydt=BF16):
-    return fn("moe_train", "moe_grouped_linear")(s, x, dt, w, off, y, ydt, None, None)
+    return fn("moe_train", "moe_grouped_linear")(s, x, dt, w, off, y, ydt, None, 0, None, None)
 
 
 def dx(s, dy=P, dt=BF16, w=P, dy2=None, w2=None, off=P, out=P, odt=BF16):
-    return fn("moe_train", "moe_grouped_linear_dx")(s, dy, dt, w, dy2, w2, off, out, odt, None, None)
+    return fn("moe_train", "moe_grouped_linear_dx")(s, dy, dt, w, dy2, w2, off, out, odt, None, 0, None,
+                                                  None)
 
 
 def dw(s, dy=P, dt=BF16, x=P, off=P, out=P, odt=BF16, acc=0):
-    return fn("moe_train", "moe_grouped_linear_dw")(s, dy, dt, x, off, out, odt, acc, None, None)
+    return fn("moe_train", "moe_grouped_linear_dw")(s, dy, dt, x, off, out, odt, acc, None, 0, None, None)
 
 
 def save(s, x=P, dt=BF16, h=P, ca=P, ws=P, nws=1 << 40):
