@@ -229,6 +229,7 @@ struct RowParams {
   int G, F;          // F: features (columns of the result)
   int kb0, kb;       // k-blocks of one pass, of all passes of all sources
   int passes;        // 1, or SPLIT_PASSES for split operands
+  int splits;        // LIN, DX: parts of the contraction, each with its own out
   int vec;           // UP, BWD: rows of the results in whole vectors of 4
   int64_t rows;
   void *out;         // LIN, DX: [rows, F]; UP: h
@@ -285,11 +286,11 @@ struct RowCfg {
 // rows from row0 on, the first nv of which belong to the tile.
 
 template <typename TO>
-__device__ __forceinline__ void finish_rows(const RowParams &p, const float (&v)[32], int fw, int row0,
-                                            int nv) {
+__device__ __forceinline__ void finish_rows(const RowParams &p, int part, const float (&v)[32], int fw,
+                                            int row0, int nv) {
   const int f = fw + threadIdx.x % 32;
   if (f >= p.F) return;
-  TO *o = static_cast<TO *>(p.out) + (size_t)row0 * p.F + f;
+  TO *o = static_cast<TO *>(p.out) + ((size_t)part * p.rows + row0) * p.F + f;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     if (j < nv) *o = from_f<TO>(v[j]);
@@ -513,7 +514,13 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
   if (CG == 2) cluster_sync();  // the pair's barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int total = tab.start[p.G];
+  // with few tiles each is computed in parts of the contraction, which other
+  // SMs take (sum_splits adds them up)
+  const int splits = (OP == LIN || OP == DX) && SEGS ? p.splits : 1;
+  const int total = tab.start[p.G] * splits, per = (p.kb + splits - 1) / splits;
+  auto whole = [&](int tile) { return splits == 1 ? tile : tile / splits; };
+  auto part_of = [&](int tile) { return splits == 1 ? 0 : tile % splits; };
+  auto blocks = [&](int tile) { return min(per, p.kb - part_of(tile) * per); };  // k-blocks of a part
 
   if (warp < 4) {
     if (C::EPI == 8) regs_low();
@@ -528,7 +535,8 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
       Ring r;
       bool ok = true;
       for (int tile = unit; ok && tile < total; tile += nunits) {
-        const Tile t = find_tile(tab, tile, p.G);
+        const Tile t = find_tile(tab, whole(tile), p.G);
+        const int nkb = blocks(tile);
         const uint64_t pol_a = t.ntt > 1 ? keep : once;
         const int brows = ((t.nvalid + 15) & ~15) / CG;  // this SM's share
         const int b0 = t.row0 + (int)rank * brows;
@@ -537,9 +545,9 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
         const uint32_t bytes = (uint32_t)(C::A_ALL + nbox * C::BOXN * BK * 2);
         // tiles that run together start at different k-blocks, which spreads
         // their reads of shared operands over L2
-        const int k0 = (t.ft * 7 + t.tt * 5) % p.kb;
+        const int k0 = splits == 1 ? (t.ft * 7 + t.tt * 5) % p.kb : part_of(tile) * per;
         int q = k0 / p.kb0, blk = k0 - q * p.kb0;  // pass (of all sources) and block of it
-        for (int i = 0; i < p.kb; ++i) {
+        for (int i = 0; i < nkb; ++i) {
           if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
             ok = false;
             break;
@@ -581,11 +589,12 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
       Ring r, acc;
       bool ok = true;
       for (int tile = unit; ok && tile < total; tile += nunits) {
-        const Tile t = find_tile(tab, tile, p.G);
+        const Tile t = find_tile(tab, whole(tile), p.G);
+        const int nkb = blocks(tile);
         const uint32_t idesc =
             idesc_bf16_f32(BM * CG, (t.nvalid + 15) & ~15) | (C::KMAJOR ? 0u : A_MN);
         uint32_t d = 0;
-        for (int kb = 0; kb < p.kb; ++kb) {
+        for (int kb = 0; kb < nkb; ++kb) {
           const bool first = kb == 0 || (SEGS && kb % SEG == 0);
           if (first) {
             if (kb > 0) {
@@ -653,7 +662,8 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
       acc.next(C::NBUF);
     };
     for (int tile = unit; tile < total; tile += nunits) {
-      const Tile t = find_tile(tab, tile, p.G);
+      const Tile t = find_tile(tab, whole(tile), p.G);
+        const int nkb = blocks(tile);
       const int fw = t.ft * C::FEAT + (int)rank * BM + q * 32;  // the warp's first feature
       if (SEGS) {
         // sum[a * NCH + ch]: chunk ch of A tile a
@@ -668,8 +678,8 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
         auto part_row = [&](int h) { return half * 32 + h / PARTS * STEP + h % PARTS * HR; };
         BwdRows ahead;  // BWD: what the next part reads, in flight
         bool ok = true;
-        for (int kb = 0; kb < p.kb; kb += SEG) {
-          if (OP == BWD && kb + SEG >= p.kb) ahead.load(p, fw, t.row0 + part_row(0), t.nvalid - part_row(0));
+        for (int kb = 0; kb < nkb; kb += SEG) {
+          if (OP == BWD && kb + SEG >= nkb) ahead.load(p, fw, t.row0 + part_row(0), t.nvalid - part_row(0));
           if (!(ok = acquire())) break;
           if (OP == BWD && kb == 0 && fw < p.F) {
             // the codes are needed after the last segment: into L2 by then
@@ -723,7 +733,7 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
           for (int i = 0; i < AT * NCH; ++i) {
             const int c0 = half * 32 + i % NCH * STEP;
             if (c0 < t.nvalid)
-              finish_rows<TO>(p, sum[i], fw + i / NCH * BM * CG, t.row0 + c0, t.nvalid - c0);
+              finish_rows<TO>(p, part_of(tile), sum[i], fw + i / NCH * BM * CG, t.row0 + c0, t.nvalid - c0);
           }
         }
       } else {
@@ -782,6 +792,22 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
   }
 }
 
+// out = the sum of the splits' planes, in order, over the rows of the groups
+// (offsets NULL: all rows).
+template <typename TO>
+__global__ void __launch_bounds__(256) sum_splits(const float *__restrict__ part, int splits,
+                                                  const int32_t *offsets, int G, int64_t rows,
+                                                  int64_t cols, TO *__restrict__ out, int accumulate) {
+  int64_t lo = 0, hi = rows;
+  if (offsets) ckpt::live_rows(offsets, G, rows, lo, hi);
+  const int64_t plane = rows * cols, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = lo * cols + (int64_t)blockIdx.x * 256 + threadIdx.x; i < hi * cols; i += step) {
+    float s = part[i];
+    for (int k = 1; k < splits; ++k) s += part[k * plane + i];
+    out[i] = from_f<TO>(accumulate ? to_f(out[i]) + s : s);
+  }
+}
+
 // dgate[row] = the sum of its terms over the feature blocks, in order.
 __global__ void __launch_bounds__(256) sum_parts(const float *__restrict__ part,
                                                  const int32_t *offsets, int G, int64_t rows,
@@ -804,6 +830,7 @@ struct DwParams {
   void *dw;
   int accumulate;
   int passes;     // 1, or SPLIT_PASSES for split operands
+  int splits;     // parts of each group's rows, each with its own dw
   int tma_store;  // rows of dw are multiples of 16 bytes, dw is 16-byte aligned
   int32_t *status;
 };
@@ -876,10 +903,10 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int ntiles = (p.n + C::FEAT - 1) / C::FEAT, ktiles = (p.k + 255) / 256;
-  const int64_t total = (int64_t)p.G * ntiles * ktiles;
+  const int64_t total = (int64_t)p.G * p.splits * ntiles * ktiles;
 
   struct Job {
-    int g, n0, k0, lo, kc;
+    int g, n0, k0, lo, kc;  // g: plane of dw, of split s and group g' s * G + g'
     int kb0, kb, tail;  // k-blocks of one pass and of all; rows of a pass's last one
     int nmma;           // columns of the MMA
     // rows of k-block b of a pass, and whether it ends inside a 16-row step
@@ -892,7 +919,14 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     const int local = (int)(tile - (int64_t)j.g * ntiles * ktiles);
     j.n0 = local / ktiles * C::FEAT;
     j.k0 = local % ktiles * 256;
-    group_bounds(p.offsets, j.g, p.rows, j.lo, j.kc, threadIdx.x == 0 ? p.status : nullptr);
+    const int split = p.splits == 1 ? 0 : j.g / p.G;
+    group_bounds(p.offsets, j.g - split * p.G, p.rows, j.lo, j.kc, threadIdx.x == 0 ? p.status : nullptr);
+    if (p.splits > 1) {  // whole k-blocks of the group's rows
+      const int part = ((j.kc + p.splits - 1) / p.splits + BK - 1) / BK * BK;
+      const int skip = min(j.kc, split * part);
+      j.lo += skip;
+      j.kc = min(part, j.kc - skip);
+    }
     j.kb0 = (j.kc + BK - 1) / BK;
     j.kb = j.kb0 * p.passes;
     j.tail = j.kc - (j.kb0 - 1) * BK;

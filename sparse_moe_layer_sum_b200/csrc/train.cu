@@ -3,6 +3,8 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "ckpt.cuh"
 #include "common.cuh"
 #include "grouped.cuh"
@@ -15,6 +17,10 @@ namespace {
 
 using grouped::bf16;
 using grouped::Table;
+
+// SMs of a B200: what the choices that size a workspace go by, without asking
+// a device
+constexpr int SMS = 148;
 
 bool act_type(moe_dtype dt) { return dt == MOE_BF16 || dt == MOE_F32; }
 size_t elem(moe_dtype dt) { return dt == MOE_F32 ? 4 : 2; }
@@ -215,12 +221,27 @@ struct Plan {
   bool direct = false, staged = false;
   int terms = 1;         // planes of a staged operand
   size_t bytes = 0;      // of the staged operands
+  int splits = 1;        // parts of the contraction that are computed apart
+  size_t part = 0;       // bytes of their fp32 planes
+  size_t total() const { return bytes + part; }
   bool tensor() const { return direct || staged; }
 };
 
-// Operands of a product with `flops` operations.  aligned: every operand is
-// 16-byte aligned (their addresses are not looked at).
-Plan plan(const Operand *ops, int n, moe_dtype dt, double flops, bool aligned) {
+// The kinds of product, and the number of operations from which staging beats
+// the CUDA cores, by operand type.  Below, the copies and their launches cost
+// more than they save; dw crosses late because its results off the pitch are
+// stored without TMA.  Measured on 28 random shapes either side, for example
+// linear, bf16: 1.2e7 12.3 (CUDA cores) / 10.6 us (staged), 2.2e8 30 / 13 us;
+// dw, bf16: 2.2e8 18.4 / 18.2 us, 8.3e8 48 / 29 us; linear, fp32: 2e8 16.6 /
+// 16.7 us, 2.1e9 122 / 61 us; backward, fp32: 9e8 52 / 86 us, 2.1e9 121 / 82 us.
+enum Kind { K_LINEAR, K_DX, K_DW, K_UP, K_BWD };
+double staging_from(Kind k, moe_dtype dt) {
+  if (dt == MOE_F32) return k == K_BWD || k == K_DW ? 1e9 : 2e8;
+  return k == K_DW ? 5e8 : k == K_BWD ? 1e8 : 1e7;
+}
+
+// aligned: every operand is 16-byte aligned (their addresses are not looked at).
+Plan plan(Kind kind, const Operand *ops, int n, moe_dtype dt, double flops, bool aligned) {
   Plan p;
   p.terms = dt == MOE_F32 ? tcg::SPLIT_TERMS : 1;
   bool fits = dt == MOE_BF16;
@@ -234,10 +255,7 @@ Plan plan(const Operand *ops, int n, moe_dtype dt, double flops, bool aligned) {
     p.bytes = 0;
     return p;
   }
-  // Below this the copies and their launches cost more than the CUDA cores'
-  // lower rate (measured: see the table of XXX)
-  constexpr double WORTH = 1e8;
-  p.staged = flops >= WORTH;
+  p.staged = flops >= staging_from(kind, dt);
   if (!p.staged) p.bytes = 0;
   return p;
 }
@@ -306,7 +324,7 @@ moe_status launch_rows(const RowJob &j) {
   p.passes = j.terms == 1 ? 1 : tcg::SPLIT_PASSES;
   p.kb0 = (j.contract + tcg::BK - 1) / tcg::BK;
   p.kb = p.kb0 * p.passes * (j.x1.p ? 2 : 1);
-  const int64_t tiles = row_tiles(s, BN) * ((j.F + C::FEAT - 1) / C::FEAT);
+  const int64_t tiles = row_tiles(s, BN) * ((j.F + C::FEAT - 1) / C::FEAT) * (p.splits ? p.splits : 1);
   return launch_persistent<tcg::rows_gemm<OP, CG, AT, BN, STAGES, SEGS, TO>>(
       C::NT, C::smem(p.G), CG, tiles, j.stream, a0, a1, b0, b1, (const tcg::RowParams)p);
 }
@@ -314,33 +332,42 @@ moe_status launch_rows(const RowJob &j) {
 // rows of a group on average
 int64_t mean_rows(const moe_grouped_shape *s) { return (s->rows + s->groups - 1) / s->groups; }
 
+// Whether tiles of bn rows by feat features are the better choice: the groups
+// are long enough to fill them, and there are enough for half the SM pairs.
+// The narrow tiles (64 rows, 128 features, one SM) read the weights once for
+// every 64 rows but keep more SMs busy.  Linear, narrow / wide: 4 groups, 1000
+// rows, 1024 x 1024: 12 / 23 us; 32 groups, 2000 rows: 18.6 / 19.9 us; dx,
+// 4 groups, 300 rows, 2048 -> 7168: 54 / 28.5 us.
+bool wide(const RowJob &j, int bn, int feat) {
+  return mean_rows(j.s) > 48 && row_tiles(j.s, bn) * ((j.F + feat - 1) / feat) >= SMS / 4;
+}
+
 template <int OP, typename TO>
 moe_status tc_rows(const RowJob &j) {
   if constexpr (sizeof(TO) == 4) {  // fp32 results: sums in segments
-    if (mean_rows(j.s) <= 48 || j.F < 256) return launch_rows<OP, 1, 1, 64, 8, true, TO>(j);
-    return launch_rows<OP, 2, 1, 256, 6, true, TO>(j);
+    if (wide(j, 256, 256)) return launch_rows<OP, 2, 1, 256, 6, true, TO>(j);
+    return launch_rows<OP, 1, 1, 64, 8, true, TO>(j);
   } else {
-    if (mean_rows(j.s) <= 48) return launch_rows<OP, 1, 1, 64, 8, false, TO>(j);
-    if (j.F < 512) return launch_rows<OP, 1, 1, 256, 4, false, TO>(j);
-    return launch_rows<OP, 2, 2, 256, 4, false, TO>(j);
+    if (wide(j, 256, 512)) return launch_rows<OP, 2, 2, 256, 4, false, TO>(j);
+    return launch_rows<OP, 1, 1, 64, 8, false, TO>(j);
   }
 }
 
 // The first matmul with its checkpoint, and the gradients of the hidden rows.
 template <typename TO>
 moe_status tc_up(const RowJob &j) {
-  if (mean_rows(j.s) <= 48 || j.F < 256) return launch_rows<tcg::UP, 1, 2, 64, 5, true, TO>(j);
-  return launch_rows<tcg::UP, 2, 2, 128, 5, true, TO>(j);
+  if (wide(j, 128, 256)) return launch_rows<tcg::UP, 2, 2, 128, 5, true, TO>(j);
+  return launch_rows<tcg::UP, 1, 2, 64, 5, true, TO>(j);
 }
 
 template <typename TO>
 moe_status tc_bwd(const RowJob &j) {
-  if (mean_rows(j.s) <= 48 || j.F < 256) return launch_rows<tcg::BWD, 1, 1, 64, 8, true, TO>(j);
-  return launch_rows<tcg::BWD, 2, 1, 256, 6, true, TO>(j);
+  if (wide(j, 256, 256)) return launch_rows<tcg::BWD, 2, 1, 256, 6, true, TO>(j);
+  return launch_rows<tcg::BWD, 1, 1, 64, 8, true, TO>(j);
 }
 
 template <typename TO, int AT>
-moe_status launch_dw(const Product &p, const Operand *ops, int terms) {
+moe_status launch_dw(const Product &p, const Operand *ops, int terms, int splits = 1) {
   using C = tcg::DwCfg<TO, AT>;
   const auto *s = p.s;
   const uint64_t rows = (uint64_t)terms * s->rows;
@@ -350,10 +377,10 @@ moe_status launch_dw(const Product &p, const Operand *ops, int terms) {
       !tensor_map(&b, ops[1].p, MOE_BF16, 0, rows, ops[1].cols, tcg::BK))
     return MOE_ERR_CUDA;
   c = a;
-  if (store && !tensor_map(&c, p.out, p.out_dt, s->groups, s->n, s->k, 32)) return MOE_ERR_CUDA;
+  if (store && !tensor_map(&c, p.out, p.out_dt, (uint64_t)splits * s->groups, s->n, s->k, 32)) return MOE_ERR_CUDA;
   const tcg::DwParams d{p.offsets, s->groups, s->n, s->k, s->rows, p.out, p.accumulate,
-                        terms == 1 ? 1 : tcg::SPLIT_PASSES, store, p.status};
-  const int64_t tiles = (int64_t)s->groups * ((s->n + C::FEAT - 1) / C::FEAT) * ((s->k + 255) / 256);
+                        terms == 1 ? 1 : tcg::SPLIT_PASSES, splits, store, p.status};
+  const int64_t tiles = (int64_t)s->groups * splits * ((s->n + C::FEAT - 1) / C::FEAT) * ((s->k + 255) / 256);
   return launch_persistent<tcg::dw_gemm<TO, AT>>(C::NT, (size_t)C::BYTES, 2, tiles, p.stream, a, b, c, d);
 }
 
@@ -401,57 +428,127 @@ int bwd_ops(const moe_grouped_shape *s, const void *dy, const void *w2, Operand 
   return 2;
 }
 
-// The plan for operands whose addresses are known; a staged one needs its
-// workspace (without it the CUDA cores do).
-Plan plan_call(const Operand *o, int n, moe_dtype dt, double flops, const void *ws, size_t ws_bytes) {
-  Plan p = plan(o, n, dt, flops, all_aligned(o, n));
-  if (p.staged && (!ws || !aligned(ws, 16) || ws_bytes < p.bytes)) p.staged = false;
+// Few tiles leave SMs idle while each works through a long contraction: it is
+// cut into parts, the partial results go to the workspace in fp32 and are
+// added in a fixed order.  Linear, one group of 200 rows, 7168 -> 2048: 42 ->
+// 29 us.  dw, one group of 4096 rows, 512 x 512: 43 -> 17 us; it takes three
+// parts of 512 rows to pay (two of 256: 8.8 -> 12.3 us).
+void split_rows_product(Plan &p, const moe_grouped_shape *s, int F, int contract, int sources) {
+  if (!p.tensor()) return;
+  const int64_t tiles = row_tiles(s, 64) * ((F + 127) / 128);
+  const int64_t kb = (int64_t)((contract + tcg::BK - 1) / tcg::BK) * sources *
+                     (p.terms == 1 ? 1 : tcg::SPLIT_PASSES);
+  // parts of a segment (8 k-blocks) at least
+  int64_t n = std::min<int64_t>({16, SMS / (tiles < 1 ? 1 : tiles), kb / 8});
+  if (n < 2) return;
+  const int64_t per = (kb + n - 1) / n;
+  n = (kb + per - 1) / per;  // none of them empty
+  p.splits = (int)n;
+  p.part = align_up((size_t)n * s->rows * F * 4, 256);
+}
+
+void split_dw_product(Plan &p, const moe_grouped_shape *s) {
+  if (!p.tensor()) return;
+  const int64_t tiles = (int64_t)s->groups * ((s->n + 255) / 256) * ((s->k + 255) / 256);
+  const int64_t n = std::min<int64_t>({16, SMS / 2 / tiles, mean_rows(s) / 512});
+  if (n < 3) return;
+  p.splits = (int)n;
+  p.part = align_up((size_t)n * s->groups * s->n * s->k * 4, 256);
+}
+
+Plan plan_product(Kind kind, const moe_grouped_shape *s, const Operand *o, int n, moe_dtype dt,
+                  int products, bool aligned) {
+  Plan p = plan(kind, o, n, dt, flops_of(s, products), aligned);
+  if (kind == K_LINEAR) split_rows_product(p, s, s->n, s->k, products);
+  if (kind == K_DX) split_rows_product(p, s, s->k, s->n, products);
+  if (kind == K_DW) split_dw_product(p, s);
   return p;
+}
+
+// The plan for operands whose addresses are known.  Without the workspace a
+// staged product runs on the CUDA cores, a direct one undivided.
+Plan plan_call(Kind kind, const moe_grouped_shape *s, const Operand *o, int n, moe_dtype dt, int products,
+               const void *ws, size_t ws_bytes) {
+  Plan p = plan_product(kind, s, o, n, dt, products, all_aligned(o, n));
+  if (p.total() && (!ws || !aligned(ws, 16) || ws_bytes < p.total())) {
+    p.staged = false;
+    p.splits = 1;
+    p.bytes = p.part = 0;
+  }
+  return p;
+}
+
+// out = the sum of the splits' planes behind the staged operands.
+moe_status join(const Plan &pl, const Product &p, int64_t rows, int64_t cols, const int32_t *offsets) {
+  const float *part = reinterpret_cast<const float *>(static_cast<const uint8_t *>(p.ws) + pl.bytes);
+  const int64_t blocks = (rows * cols + 255) / 256, most = SMS * 8;
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  if (p.out_dt == MOE_F32)
+    tcg::sum_splits<<<grid, 256, 0, p.stream>>>(part, pl.splits, offsets, p.s->groups, rows, cols, static_cast<float *>(p.out), p.accumulate);
+  else
+    tcg::sum_splits<<<grid, 256, 0, p.stream>>>(part, pl.splits, offsets, p.s->groups, rows, cols, static_cast<bf16 *>(p.out), p.accumulate);
+  return launch_status();
+}
+
+template <int OP>
+moe_status run_rows(const Plan &pl, const Product &p, RowJob &j) {
+  j.p.offsets = p.offsets;
+  j.p.status = p.status;
+  j.p.splits = pl.splits;
+  j.p.out = p.out;
+  if (pl.splits > 1) {
+    j.p.out = static_cast<uint8_t *>(p.ws) + pl.bytes;
+    const moe_status st = launch_rows<OP, 1, 1, 64, 8, true, float>(j);
+    return st != MOE_OK ? st : join(pl, p, p.s->rows, j.F, p.offsets);
+  }
+  return p.out_dt == MOE_F32 ? tc_rows<OP, float>(j) : tc_rows<OP, bf16>(j);
 }
 
 moe_status run_linear(const Product &p) {
   Operand o[4];
   const int n = linear_ops(p.s, p.a0, p.b0, o);
-  const Plan pl = plan_call(o, n, p.dt, flops_of(p.s, 1), p.ws, p.ws_bytes);
+  const Plan pl = plan_call(K_LINEAR, p.s, o, n, p.dt, 1, p.ws, p.ws_bytes);
   if (!pl.tensor()) return simt_product<simt::LIN>(simt_args(p), p.dt, p.out_dt, p.stream);
   if (pl.staged) {
     const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
     if (st != MOE_OK) return st;
   }
   RowJob j{p.s, p.s->n, p.s->k, pl.terms, o[0], o[1], {}, {}, {}, p.stream};
-  j.p.offsets = p.offsets;
-  j.p.out = p.out;
-  j.p.status = p.status;
-  return p.out_dt == MOE_F32 ? tc_rows<tcg::LIN, float>(j) : tc_rows<tcg::LIN, bf16>(j);
+  return run_rows<tcg::LIN>(pl, p, j);
 }
 
 moe_status run_dx(const Product &p) {
   Operand o[4];
   const bool two = p.a1 != nullptr;
   const int n = dx_ops(p.s, p.a0, p.b0, p.a1, p.b1, two, o);
-  const Plan pl = plan_call(o, n, p.dt, flops_of(p.s, two ? 2 : 1), p.ws, p.ws_bytes);
+  const Plan pl = plan_call(K_DX, p.s, o, n, p.dt, two ? 2 : 1, p.ws, p.ws_bytes);
   if (!pl.tensor()) return simt_product<simt::DX>(simt_args(p), p.dt, p.out_dt, p.stream);
   if (pl.staged) {
     const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
     if (st != MOE_OK) return st;
   }
   RowJob j{p.s, p.s->k, p.s->n, pl.terms, o[0], o[1], o[2], o[3], {}, p.stream};
-  j.p.offsets = p.offsets;
-  j.p.out = p.out;
-  j.p.status = p.status;
-  return p.out_dt == MOE_F32 ? tc_rows<tcg::DX, float>(j) : tc_rows<tcg::DX, bf16>(j);
+  return run_rows<tcg::DX>(pl, p, j);
 }
 
 moe_status run_dw(const Product &p) {
   Operand o[4];
   const int n = dw_ops(p.s, p.a0, p.b0, o);
-  const Plan pl = plan_call(o, n, p.dt, flops_of(p.s, 1), p.ws, p.ws_bytes);
+  const Plan pl = plan_call(K_DW, p.s, o, n, p.dt, 1, p.ws, p.ws_bytes);
   // without rows there is nothing to map; the CUDA-core kernel writes the zeros
   if (!pl.tensor() || p.s->rows == 0)
     return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
   if (pl.staged) {
     const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
     if (st != MOE_OK) return st;
+  }
+  if (pl.splits > 1) {
+    Product q = p;
+    q.out = static_cast<uint8_t *>(p.ws) + pl.bytes;
+    q.out_dt = MOE_F32;
+    q.accumulate = 0;
+    const moe_status st = launch_dw<float, 1>(q, o, pl.terms, pl.splits);
+    return st != MOE_OK ? st : join(pl, p, (int64_t)p.s->groups * p.s->n, p.s->k, nullptr);
   }
   return tc_dw(p, o, pl.terms);
 }
@@ -460,7 +557,7 @@ int scale_blocks(int n) { return (n + ckpt::BLOCK - 1) / ckpt::BLOCK; }
 
 unsigned row_grid(int64_t warps) {
   const int64_t blocks = (warps + ckpt::ROW_THREADS / 32 - 1) / (ckpt::ROW_THREADS / 32);
-  const int64_t most = 148 * 8;
+  const int64_t most = SMS * 8;
   return (unsigned)(blocks < most ? blocks : most);
 }
 
@@ -473,7 +570,8 @@ MOE_EXPORT size_t moe_grouped_linear_workspace_size(const moe_grouped_shape *s, 
                                                     int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
-  return plan(o, linear_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned).bytes;
+  const int n = linear_ops(s, nullptr, nullptr, o);
+  return plan_product(K_LINEAR, s, o, n, dt, 1, aligned).total();
 }
 
 MOE_EXPORT size_t moe_grouped_linear_dx_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
@@ -481,14 +579,15 @@ MOE_EXPORT size_t moe_grouped_linear_dx_workspace_size(const moe_grouped_shape *
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
   const int n = dx_ops(s, nullptr, nullptr, nullptr, nullptr, two != 0, o);
-  return plan(o, n, dt, flops_of(s, two ? 2 : 1), aligned).bytes;
+  return plan_product(K_DX, s, o, n, dt, two ? 2 : 1, aligned).total();
 }
 
 MOE_EXPORT size_t moe_grouped_linear_dw_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
                                                        int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
-  return plan(o, dw_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned).bytes;
+  const int n = dw_ops(s, nullptr, nullptr, o);
+  return plan_product(K_DW, s, o, n, dt, 1, aligned).total();
 }
 
 MOE_EXPORT moe_status moe_grouped_linear(const moe_grouped_shape *s, const void *x, moe_dtype dt,
@@ -591,7 +690,7 @@ MOE_EXPORT size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *
                                                        int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
-  const Plan p = plan(o, up_ops(s, nullptr, nullptr, nullptr, o), dt, flops_of(s, 2), aligned);
+  const Plan p = plan(K_UP, o, up_ops(s, nullptr, nullptr, nullptr, o), dt, flops_of(s, 2), aligned);
   // on the CUDA cores: the two projections in fp32
   return p.tensor() ? p.bytes : 2 * align_up((size_t)s->rows * s->n * 4, 256);
 }
@@ -613,7 +712,7 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
   Operand o[4];
   const int n = up_ops(s, x, w1, w3, o);
   const bool fits = all_aligned(o, n);
-  const Plan p = plan(o, n, dt, flops_of(s, 2), fits);
+  const Plan p = plan(K_UP, o, n, dt, flops_of(s, 2), fits);
   const size_t need = moe_swiglu_checkpoint_workspace_size(s, dt, fits);
   if (need && (!ws || !aligned(ws, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   if (p.tensor()) {
@@ -649,7 +748,7 @@ MOE_EXPORT size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s,
                                                      int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
-  const Plan p = plan(o, bwd_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned);
+  const Plan p = plan(K_BWD, o, bwd_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned);
   return p.tensor() ? part_bytes(s) + p.bytes : (size_t)s->rows * s->n * 4;  // else dh in fp32
 }
 
@@ -673,7 +772,7 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
   Operand o[4];
   const int n = bwd_ops(s, dy, w2, o);
   const bool fits = all_aligned(o, n);
-  const Plan p = plan(o, n, dt, flops_of(s, 1), fits);
+  const Plan p = plan(K_BWD, o, n, dt, flops_of(s, 1), fits);
   if (!ws || !aligned(ws, 16) || ws_bytes < moe_swiglu_backward_workspace_size(s, dt, fits))
     return MOE_ERR_WORKSPACE;
   if (p.tensor()) {

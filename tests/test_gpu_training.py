@@ -23,6 +23,11 @@ SHAPES = [
     # large enough for the tensor cores although off their alignment
     ([300, 0, 513, 1, 17], 333, 301),
     ([21, 33, 90, 40, 64, 15, 77, 8, 130, 1], 607, 449),
+    # few tiles with a long contraction, which is cut into parts
+    ([5, 0, 40], 96, 2504),
+    ([3], 2056, 72),
+    ([0, 2900, 1800], 72, 64),
+    ([900, 6], 100, 1302),
 ]
 
 
