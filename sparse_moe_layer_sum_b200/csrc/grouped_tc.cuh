@@ -408,7 +408,8 @@ struct BwdRows {
   uint32_t ca[4], cu[4];
   int e[4];
   float g[4];
-  __device__ __forceinline__ void load(const RowParams &p, int fw, int row0, int nv) {
+  template <bool VEC>
+  __device__ __forceinline__ void load_as(const RowParams &p, int fw, int row0, int nv) {
     const int lane = threadIdx.x % 32, f = fw + lane % 8 * 4;
     const int nb = (p.F + ckpt::BLOCK - 1) / ckpt::BLOCK;
 #pragma unroll
@@ -419,12 +420,20 @@ struct BwdRows {
       g[s] = 1.0f;
       if (r < nv && f < p.F) {
         const size_t at = (size_t)(row0 + r) * p.F + f, sat = (size_t)(row0 + r) * nb + fw / ckpt::BLOCK;
-        ca[s] = get4_codes(p.saved.ca + at, p.F - f, p.vec);
-        cu[s] = get4_codes(p.saved.cu + at, p.F - f, p.vec);
+        ca[s] = get4_codes(p.saved.ca + at, p.F - f, VEC);
+        cu[s] = get4_codes(p.saved.cu + at, p.F - f, VEC);
         e[s] = __ldg(p.saved.ea + sat) | __ldg(p.saved.eu + sat) << 8;
         if (p.gate) g[s] = __ldg(p.gate + row0 + r);
       }
     }
+  }
+  // (one branch around all loads: a branch at each kept them from being in
+  // flight together and cost 7% of the call)
+  __device__ __forceinline__ void load(const RowParams &p, int fw, int row0, int nv) {
+    if (p.vec)
+      load_as<true>(p, fw, row0, nv);
+    else
+      load_as<false>(p, fw, row0, nv);
   }
 };
 
@@ -438,22 +447,33 @@ __device__ __forceinline__ void finish_bwd(const RowParams &p, const BwdRows &in
     const float4 d4 = *reinterpret_cast<const float4 *>(x + r * 32 + lane % 8 * 4);
     const float dh[4] = {d4.x, d4.y, d4.z, d4.w};
     const float sa = ckpt::scale_of(in.e[s] & 0xff), su = ckpt::scale_of(in.e[s] >> 8);
-    float da[4], du[4], hg[4], term = 0.0f;
+    float da[4], du[4], hg[4], t[4];
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       const float2 a = ckpt::decode2((uint16_t)(in.ca[s] >> (8 * i))), u = ckpt::decode2((uint16_t)(in.cu[s] >> (8 * i)));
-      const float t0 = ckpt::swiglu_grad<TO>(a.x * sa, u.x * su, dh[i], in.g[s], da[i], du[i], hg[i]);
-      const float t1 = ckpt::swiglu_grad<TO>(a.y * sa, u.y * su, dh[i + 1], in.g[s], da[i + 1], du[i + 1], hg[i + 1]);
-      if (r < nv && f + i < p.F) term += t0;
-      if (r < nv && f + i + 1 < p.F) term += t1;
+      t[i] = ckpt::swiglu_grad<TO>(a.x * sa, u.x * su, dh[i], in.g[s], da[i], du[i], hg[i]);
+      t[i + 1] = ckpt::swiglu_grad<TO>(a.y * sa, u.y * su, dh[i + 1], in.g[s], da[i + 1], du[i + 1], hg[i + 1]);
     }
+    if (!p.vec) {  // features behind the last: not in the sum even where dy is not finite
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (f + i >= p.F) t[i] = 0.0f;
+    }
+    const bool on = r < nv && f < p.F;
+    float term = on ? (t[0] + t[1]) + (t[2] + t[3]) : 0.0f;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-    if (r >= nv || f >= p.F) continue;
+    if (!on) continue;
     const size_t at = (size_t)(row0 + r) * p.F + f;
-    put4<TO>(p.da, at, da, p.F - f, p.vec);
-    put4<TO>(p.du, at, du, p.F - f, p.vec);
-    put4<TO>(p.hg, at, hg, p.F - f, p.vec);
+    if (p.vec) {
+      put4<TO>(p.da, at, da, 4, true);
+      put4<TO>(p.du, at, du, 4, true);
+      put4<TO>(p.hg, at, hg, 4, true);
+    } else {
+      put4<TO>(p.da, at, da, p.F - f, false);
+      put4<TO>(p.du, at, du, p.F - f, false);
+      put4<TO>(p.hg, at, hg, p.F - f, false);
+    }
     if (lane % 8 == 0) p.part[(size_t)(fw / ckpt::BLOCK) * p.rows + row0 + r] = term;
   }
 }

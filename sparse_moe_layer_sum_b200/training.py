@@ -54,13 +54,14 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _check(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
-    dev = first.device
-    for t in (first, *others):
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
-            raise ValueError("tensors must be contiguous CUDA tensors")
-        if t is not None and t.device != dev:
-            raise ValueError("tensors must be on one device")
+def _check(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The CUDA device of all of them (an index)."""
+    dev = first.get_device()
+    if dev < 0 or not first.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    for t in others:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and on one CUDA device")
     return dev
 
 
@@ -74,17 +75,16 @@ def _entry(sym: str):
     return f
 
 
-def _call(dev: torch.device, sym: str, *args) -> None:
+def _call(dev: int, sym: str, *args) -> None:
     """Call `sym` of moe_train with `dev` current, on its current stream.  (The
     raw stream handle is read directly: torch.cuda.current_stream() alone takes
     as long as the rest of a call.)"""
     f = _entry(sym)
-    i = dev.index
-    if i == torch._C._cuda_getDevice():
-        st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if dev == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         check(st, sym)
 
@@ -96,13 +96,19 @@ def _groups(offsets: torch.Tensor) -> int:
 
 
 def _dtype(t: torch.Tensor, *others: torch.Tensor) -> int:
-    _need(t.dtype in _DT, "operands must be bf16 or fp32")
-    _need(all(o.dtype == t.dtype for o in others), "operands must have one dtype")
-    return _DT[t.dtype]
+    d = t.dtype
+    dt = _DT.get(d)
+    if dt is None:
+        raise ValueError("operands must be bf16 or fp32")
+    for o in others:
+        if o.dtype != d:
+            raise ValueError("operands must have one dtype")
+    return dt
 
 
-def _out(out, shape, dtype, dev) -> torch.Tensor:
-    _need(dtype in _DT, "outputs must be bf16 or fp32")
+def _out(out, shape, dtype, dev: int) -> torch.Tensor:
+    if dtype not in _DT:
+        raise ValueError("outputs must be bf16 or fp32")
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     _need(tuple(out.shape) == tuple(shape) and out.dtype == dtype, "out has another shape or dtype")
@@ -115,10 +121,21 @@ def _status(status: Optional[torch.Tensor]) -> Optional[int]:
     return _ptr(status)
 
 
+_bytes: dict = {}  # workspace sizes by what they depend on
+
+
 def _workspace(sym: str, shape: MoEGroupedShape, dt: int, dev, operands, *flags: int):
     """(tensor or None, address or None, bytes) of the workspace `sym` asks for."""
-    aligned = not any(t.data_ptr() % 16 for t in operands)
-    need = _entry(sym)(ctypes.byref(shape), dt, *flags, int(aligned))
+    aligned = 1
+    for t in operands:
+        if t.data_ptr() & 15:
+            aligned = 0
+    key = (sym, shape.groups, shape.n, shape.k, shape.rows, dt, aligned, *flags)
+    need = _bytes.get(key)
+    if need is None:
+        if len(_bytes) > 4096:
+            _bytes.clear()
+        need = _bytes[key] = _entry(sym)(ctypes.byref(shape), dt, *flags, aligned)
     if not need:
         return None, None, 0
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
