@@ -82,12 +82,14 @@ def test_products(sizes, n, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("n,k", [(128, 256), (520, 264), (33, 77)])
-def test_rows_outside_the_groups_stay(n, k, dtype):
+@pytest.mark.parametrize("n,k,sizes", [(128, 256, [21, 0, 70, 9]), (520, 264, [21, 0, 70, 9]),
+                                       (33, 77, [21, 0, 70, 9]), (520, 264, [210, 0, 700, 90]),
+                                       (607, 449, [210, 0, 700, 90]), (40, 1600, [21, 0, 70, 9])])
+def test_rows_outside_the_groups_stay(n, k, sizes, dtype):
     """Rows before the first and behind the last group are left as they were,
     and what they hold (NaN here) reaches no result; neither does a NaN in
     another group's rows or weights."""
-    off = R.offsets_of([21, 0, 70, 9], first=3)
+    off = R.offsets_of(sizes, first=3)
     rows, G = off[-1] + 40, 4
     x, dy = R.normal(1, rows, k, dtype=dtype), R.normal(2, rows, n, dtype=dtype)
     w = R.normal(3, G, n, k, dtype=dtype, std=k ** -0.5)
@@ -116,6 +118,134 @@ def test_rows_outside_the_groups_stay(n, k, dtype):
     keep = [0, 1, 3]
     R.assert_close(g[keep], want[keep], e[keep])
     assert torch.isnan(g[2]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_groups(dtype):
+    """The most groups there can be, most of them empty or of a row or two."""
+    G, n, k = 1024, 64, 72
+    g = torch.Generator().manual_seed(4)
+    sizes = torch.randint(-6, 5, (G,), generator=g).clamp_min(0).tolist()
+    sizes[17], sizes[1023] = 130, 70
+    off = R.offsets_of(sizes)
+    x, dy = R.normal(1, off[-1], k, dtype=dtype), R.normal(2, off[-1], n, dtype=dtype)
+    w = R.normal(3, G, n, k, dtype=dtype)
+    xd, dyd, wd = dev(x, dy, w)
+    o, st = offs(off), status()
+    R.assert_close(moe.grouped_linear(xd, wd, o, status=st), *R.linear(x, w, off))
+    R.assert_close(moe.grouped_linear_dx(dyd, wd, o, status=st), *R.dx(dy, w, off))
+    R.assert_close(moe.grouped_linear_dw(dyd, xd, o, status=st), *R.dw(dy, x, off))
+    h, a, u = moe.swiglu_checkpoint(xd, wd, wd, o, status=st)
+    got = moe.swiglu_backward(xd, wd.transpose(1, 2).contiguous(), a, u, o, status=st)
+    assert int(st.item()) == 0
+    dh, e = R.dx(x, w.transpose(1, 2), off)
+    av, uv = (R.decode(c.codes.cpu(), c.exps.cpu()) for c in (a, u))
+    for t, v, b in zip(got, *R.swiglu_grads(av, uv, dh, e, torch.ones(off[-1], dtype=R.F64), dtype)):
+        R.assert_close(t, v, b)
+
+
+def shifted(t):
+    """t's values at an address one element off a fresh allocation's."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    v = buf[1:].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16
+    return v
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sizes,n,k", [([5, 70], 64, 128), ([300, 0, 290], 520, 328)])
+def test_misaligned_operands(sizes, n, k, dtype):
+    off = R.offsets_of(sizes)
+    rows, G = off[-1], len(sizes)
+    x, dy = R.normal(1, rows, k, dtype=dtype), R.normal(2, rows, n, dtype=dtype)
+    w = R.normal(3, G, n, k, dtype=dtype, std=k ** -0.5)
+    xd, dyd, wd = shifted(x), shifted(dy), shifted(w)
+    o = offs(off)
+    y = shifted(torch.zeros(rows, n, dtype=dtype))
+    R.assert_close(moe.grouped_linear(xd, wd, o, out=y), *R.linear(x, w, off))
+    R.assert_close(moe.grouped_linear_dx(dyd, wd, o), *R.dx(dy, w, off))
+    g = shifted(torch.zeros(G, n, k, dtype=dtype))
+    R.assert_close(moe.grouped_linear_dw(dyd, xd, o, out=g), *R.dw(dy, x, off))
+    # results at odd addresses from aligned operands
+    R.assert_close(moe.grouped_linear(x.cuda(), w.cuda(), o, out=y), *R.linear(x, w, off))
+    R.assert_close(moe.grouped_linear_dw(dy.cuda(), x.cuda(), o, out=g), *R.dw(dy, x, off))
+    h, a, u = moe.swiglu_checkpoint(xd, wd, wd, o)
+    want = moe.swiglu_checkpoint(x.cuda(), w.cuda(), w.cuda(), o)
+    R.assert_close(h, want[0].cpu().to(R.F64), 2 * R.HALF[dtype] * want[0].cpu().to(R.F64).abs() +
+                   1e-5)  # two roundings, and two sums of unit-variance terms
+    a = moe.Checkpoint(shifted(a.codes), shifted(a.exps))
+    w2 = R.normal(4, G, k, n, dtype=dtype, std=n ** -0.5)
+    got = moe.swiglu_backward(xd, shifted(w2), a, u, o)
+    dh, e = R.dx(x, w2, off)
+    av, uv = (R.decode(c.codes.cpu(), c.exps.cpu()) for c in (a, u))
+    for t, v, b in zip(got, *R.swiglu_grads(av, uv, dh, e, torch.ones(rows, dtype=R.F64), dtype)):
+        R.assert_close(t, v, b)
+
+
+def test_results_past_32_bit_offsets():
+    """More than 2^31 elements in a result; the rows around that mark."""
+    n, k, rows = 8192, 64, 270000
+    x, w = R.normal(1, 3000, k), R.normal(2, 3, n, k, std=k ** -0.5)
+    off = [0, 1000, 262000, rows]
+    idx = (torch.arange(rows) % 3000).int()
+    xd, wd = moe.gather_rows(x.cuda(), idx.cuda()), w.cuda()
+    y = moe.grouped_linear(xd, wd, offs(off))
+    at = torch.tensor([0, 999, 1000, 261999, 262000, 262143, 262144, 262145, rows - 1])
+    assert rows * n > 2 ** 31 and (262144 * n == 2 ** 31)
+    for i in at.tolist():
+        g = sum(i >= o for o in off) - 1
+        v, e = R.linear(x[idx[i].long()][None], w[g][None], [0, 1])
+        R.assert_close(y[i][None], v, e, f"row {i}")
+    c = moe.checkpoint_rows(y)
+    r = moe.restore_rows(c)
+    exps = R.scale_exps(y[at.cuda()].cpu())
+    assert torch.equal(c.exps[at.cuda()].cpu(), exps)
+    assert torch.equal(r[at.cuda()].cpu().to(R.F64), R.decode(c.codes[at.cuda()].cpu(), exps))
+    del c, r
+    dxr = moe.grouped_linear_dx(y, wd, offs(off))             # reads past the mark
+    for i in at.tolist()[-3:]:
+        v, e = R.dx(y[i][None].cpu(), w[2][None], [0, 1])
+        R.assert_close(dxr[i][None], v, e, f"dx row {i}")
+    del y, dxr
+    # a weight gradient with its last matrices past the mark
+    G, n, k = 33, 8192, 8192
+    dy, x = R.normal(3, 99, n), R.normal(4, 99, k)
+    dw = moe.grouped_linear_dw(dy.cuda(), x.cuda(), offs([3 * g for g in range(G + 1)]))
+    assert dw.numel() > 2 ** 31
+    for g in (0, 31, 32):
+        v, e = R.dw(dy[3 * g:3 * g + 3], x[3 * g:3 * g + 3], [0, 3])
+        R.assert_close(dw[g, -300:, -300:][None], v[:, -300:, -300:], e[:, -300:, -300:])
+
+
+@pytest.mark.parametrize("dtype,sizes", [(BF, [300, 0, 513, 1, 17]), (F32, [300, 0, 513, 1, 17]),
+                                         (F32, [400, 3, 700, 0, 17])])
+def test_without_a_workspace(dtype, sizes):
+    """The C entry points without a workspace: the CUDA cores do it."""
+    import ctypes
+    from sparse_moe_layer_sum_b200._lib import MoEGroupedShape, fn
+    n, k = 333, 301
+    off = R.offsets_of(sizes)
+    rows, G = off[-1], len(sizes)
+    x, dy = R.normal(1, rows, k, dtype=dtype), R.normal(2, rows, n, dtype=dtype)
+    w = R.normal(3, G, n, k, dtype=dtype, std=k ** -0.5)
+    xd, dyd, wd = dev(x, dy, w)
+    o, dt = offs(off), int(dtype == BF)
+    s = ctypes.byref(MoEGroupedShape(G, n, k, rows))
+    if dtype == BF or rows > 1000:  # sizes for which one is asked for
+        assert fn("moe_train", "moe_grouped_linear_workspace_size")(s, dt, 1) > 0
+    stream = torch.cuda.current_stream().cuda_stream
+    y, d, g = (torch.empty(*t, dtype=dtype, device="cuda") for t in ((rows, n), (rows, k), (G, n, k)))
+    assert fn("moe_train", "moe_grouped_linear")(s, xd.data_ptr(), dt, wd.data_ptr(), o.data_ptr(),
+                                                 y.data_ptr(), dt, None, 0, None, stream) == 0
+    assert fn("moe_train", "moe_grouped_linear_dx")(s, dyd.data_ptr(), dt, wd.data_ptr(), None, None,
+                                                    o.data_ptr(), d.data_ptr(), dt, None, 0, None,
+                                                    stream) == 0
+    assert fn("moe_train", "moe_grouped_linear_dw")(s, dyd.data_ptr(), dt, xd.data_ptr(), o.data_ptr(),
+                                                    g.data_ptr(), dt, 0, None, 0, None, stream) == 0
+    R.assert_close(y, *R.linear(x, w, off))
+    R.assert_close(d, *R.dx(dy, w, off))
+    R.assert_close(g, *R.dw(dy, x, off))
 
 
 # ---------------------------------------------------------------- 8-bit rows

@@ -96,6 +96,27 @@ def test_no_rows_launch_nothing():
     assert save(s, x=None) == 0 and back(s, dy=None) == 0
 
 
+def test_workspaces():
+    size = lambda name, *a: fn("moe_train", f"moe_{name}_workspace_size")(*a)
+    s, big = shape(), shape(rows=4000, n=1000, k=1000)
+    odd = shape(rows=4000, n=1001, k=1001)
+    # operands that are read as they are need none; fp32 and odd ones do
+    assert size("grouped_linear", big, BF16, 1) == size("grouped_linear_dw", big, BF16, 1) == 0
+    assert size("grouped_linear_dx", big, BF16, 1, 1) == size("swiglu_checkpoint", big, BF16, 1) == 0
+    for args in ((big, F32, 1), (odd, BF16, 1), (big, BF16, 0)):
+        assert size("grouped_linear", *args) > 0 and size("swiglu_checkpoint", *args) > 0
+        assert size("grouped_linear_dw", *args) > 0
+        one, two = (size("grouped_linear_dx", args[0], args[1], t, args[2]) for t in (0, 1))
+        assert two > one > 0
+    assert size("swiglu_backward", s, BF16, 1) >= 10 * 2 * 4     # a term for 32 features of a row
+    for name in ("grouped_linear", "grouped_linear_dw", "swiglu_checkpoint", "swiglu_backward"):
+        assert size(name, shape(groups=0), BF16, 1) == size(name, s, E4M3, 1) == 0
+    # too small or off its alignment
+    assert back(s, nws=16) == WORKSPACE and back(s, ws=None) == WORKSPACE
+    assert back(s, ws=ctypes.c_void_p(0x1004)) == WORKSPACE
+    assert save(s, dt=F32, nws=16) == WORKSPACE and save(s, dt=F32, ws=None) == WORKSPACE
+
+
 def test_rows_refusals():
     sv, ld = fn("moe_train", "moe_checkpoint_rows"), fn("moe_train", "moe_restore_rows")
     assert sv(P, BF16, -1, 8, P, P, None) == INVALID
