@@ -194,7 +194,14 @@ moe_status launch_persistent(int threads, size_t smem, int cg, int64_t tiles,
   if (n < units) units = n;
   if (tiles < units) units = tiles > 0 ? tiles : 1;
   cfg.gridDim = dim3((unsigned)(units * cg));
-  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    // a device that was reset has forgotten the shared-memory limit
+    cudaGetLastError();
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) !=
+            cudaSuccess ||
+        cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
   return launch_status();
 }
 

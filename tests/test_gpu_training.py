@@ -23,6 +23,8 @@ SHAPES = [
     # large enough for the tensor cores although off their alignment
     ([300, 0, 513, 1, 17], 333, 301),
     ([21, 33, 90, 40, 64, 15, 77, 8, 130, 1], 607, 449),
+    ([700, 0, 900, 33], 607, 537),
+    ([700, 0, 900, 33], 640, 520),
     # few tiles with a long contraction, which is cut into parts
     ([5, 0, 40], 96, 2504),
     ([3], 2056, 72),
@@ -246,6 +248,23 @@ def test_without_a_workspace(dtype, sizes):
     R.assert_close(y, *R.linear(x, w, off))
     R.assert_close(d, *R.dx(dy, w, off))
     R.assert_close(g, *R.dw(dy, x, off))
+
+
+def test_infinite_operands_stay_in_their_rows():
+    """fp32 operands in three terms: rows that meet an infinity are not finite,
+    the others are as without it."""
+    off = R.offsets_of([300, 500])
+    x, w = R.normal(1, 800, 520, dtype=F32), R.normal(2, 2, 640, 520, dtype=F32)
+    bad = x.clone()
+    bad[7, 3], bad[401, 0], bad[500, 519] = float("inf"), float("-inf"), float("nan")
+    bad[600, 5] = 3.4e38                     # rounds to infinity in bf16, but is not
+    y = moe.grouped_linear(bad.cuda(), w.cuda(), offs(off)).cpu()
+    hit = torch.zeros(800, dtype=torch.bool)
+    hit[[7, 401, 500]] = True
+    assert not torch.isfinite(y[hit]).any()
+    hit[600] = True
+    v, e = R.linear(x, w, off)
+    R.assert_close(y[~hit], v[~hit], e[~hit])
 
 
 # ---------------------------------------------------------------- 8-bit rows
