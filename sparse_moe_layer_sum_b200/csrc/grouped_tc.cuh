@@ -247,6 +247,19 @@ struct RowParams {
 // it; fp32 ones, and 8-bit codes next to a rounding border, do.
 constexpr int SEG = 512 / BK;
 
+// k-blocks of the i-th segment of a tile of nkb.  BWD ends a tile with
+// arithmetic that takes the MMAs of several segments, and the MMAs may run two
+// segments ahead of it: in a long contraction its first two are twice as long
+// (636 -> 596 us over 32 groups, 16384 rows; error 6e-7 instead of 5e-7).
+// UP's codes change with the sums' last bits near a border; over a short
+// contraction, where plain fp32 sums are better than that, its segments are
+// half as long.
+template <int OP>
+__device__ __forceinline__ int segment(int i, int nkb) {
+  if (OP == UP && nkb <= 32) return SEG / 2;
+  return OP == BWD && i < 2 && nkb >= 64 ? 2 * SEG : SEG;
+}
+
 // CG: SMs per tile.  AT: A tiles per SM (UP: one of w1 and the same rows of
 // w3; LIN, DX: two blocks of features, which halves the row bytes each weight
 // byte is paired with).  BN: rows of a tile.  SEGS: sums in segments; the
@@ -614,9 +627,11 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
         const uint32_t idesc =
             idesc_bf16_f32(BM * CG, (t.nvalid + 15) & ~15) | (C::KMAJOR ? 0u : A_MN);
         uint32_t d = 0;
+        int seg = 0, cut = 0;  // segments begun, the k-block that begins the next
         for (int kb = 0; kb < nkb; ++kb) {
-          const bool first = kb == 0 || (SEGS && kb % SEG == 0);
+          const bool first = SEGS ? kb == cut : kb == 0;
           if (first) {
+            if (SEGS) cut += segment<OP>(seg++, nkb);
             if (kb > 0) {
               commit<CG>(accf + acc.stage);
               acc.next(C::NBUF);
@@ -698,8 +713,8 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
         auto part_row = [&](int h) { return half * 32 + h / PARTS * STEP + h % PARTS * HR; };
         BwdRows ahead;  // BWD: what the next part reads, in flight
         bool ok = true;
-        for (int kb = 0; kb < nkb; kb += SEG) {
-          if (OP == BWD && kb + SEG >= nkb) ahead.load(p, fw, t.row0 + part_row(0), t.nvalid - part_row(0));
+        for (int kb = 0, seg = 0; kb < nkb; kb += segment<OP>(seg++, nkb)) {
+          if (OP == BWD && kb + segment<OP>(seg, nkb) >= nkb) ahead.load(p, fw, t.row0 + part_row(0), t.nvalid - part_row(0));
           if (!(ok = acquire())) break;
           if (OP == BWD && kb == 0 && fw < p.F) {
             // the codes are needed after the last segment: into L2 by then
