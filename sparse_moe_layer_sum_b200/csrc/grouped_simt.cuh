@@ -34,6 +34,7 @@ struct Args {
   int G, n, k;
   int64_t rows;
   int accumulate;  // DW
+  int splits;      // parts of the contraction, each with its own plane of c
   int32_t *status;
 };
 
@@ -73,12 +74,16 @@ __global__ void __launch_bounds__(THREADS, Cfg<T>::BLOCKS) product(Args p) {
   const int cols = DIR == LIN ? p.n : p.k;  // columns of C
   const int ftiles = (cols + T - 1) / T, rtiles = (p.n + T - 1) / T;
   build_table(tab, p.offsets, p.G, p.rows, ftiles, p.status);
-  const int64_t tiles = DIR == DW ? (int64_t)p.G * rtiles * ftiles : tab.start[p.G];
+  const int64_t whole = DIR == DW ? (int64_t)p.G * rtiles * ftiles : tab.start[p.G];
+  const int splits = T == 32 ? p.splits : 1;
+  const int64_t tiles = whole * splits;
   const int tid = threadIdx.x, grp = tid / (NT * NT), tx = tid % NT, ty = tid / NT % NT;
   // a thread's values: TT = 8 takes two runs of four, half a tile apart
   auto at = [&](int t, int i) { return i / 4 * (T / 2) + t * 4 + i % 4; };
 
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  for (int64_t at_tile = blockIdx.x; at_tile < tiles; at_tile += gridDim.x) {
+    const int part = splits == 1 ? 0 : (int)(at_tile % splits);
+    const int64_t tile = splits == 1 ? at_tile : at_tile / splits;
     // C's rows r0 .. r0 + nr - 1 and columns from c0; the contraction runs
     // over [k0, k0 + kc)
     int g, nr, c0, kc;
@@ -142,9 +147,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<T>::BLOCKS) product(Args p) {
         Bm += b_step;
       }
     };
-    const int total = slices * nsrc;
-    if (total > 0) load(0);
-    for (int sl = 0; sl < total; ++sl) {
+    const int per = splits == 1 ? slices * nsrc : (slices * nsrc + splits - 1) / splits, begin = part * per;
+    const int total = min(slices * nsrc, begin + per);
+    if (begin < total) load(begin);
+    for (int sl = begin; sl < total; ++sl) {
       float *As = smem + sl % 2 * C::BUF, *Bs = As + BK * PITCH;
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
@@ -180,22 +186,23 @@ __global__ void __launch_bounds__(THREADS, Cfg<T>::BLOCKS) product(Args p) {
       for (int j = 0; j < TT / 2; ++j) unpair(acc[i][j], sum[i][2 * j], sum[i][2 * j + 1]);
     __syncthreads();  // the buffers are free: the next tile's, or the partial tiles'
     if (C::GROUPS > 1) {
-      float *part = smem + (tid % (NT * NT)) * TT * TT;  // of this thread's values
+      float *mine = smem + (tid % (NT * NT)) * TT * TT;  // of this thread's values
       for (int q = 1; q < C::GROUPS; ++q) {
         if (grp == q) {
 #pragma unroll
-          for (int i = 0; i < TT * TT; ++i) part[i] = sum[i / TT][i % TT];
+          for (int i = 0; i < TT * TT; ++i) mine[i] = sum[i / TT][i % TT];
         }
         __syncthreads();
         if (grp == 0) {
 #pragma unroll
-          for (int i = 0; i < TT * TT; ++i) sum[i / TT][i % TT] += part[i];
+          for (int i = 0; i < TT * TT; ++i) sum[i / TT][i % TT] += mine[i];
         }
         __syncthreads();
       }
       if (grp != 0) continue;
     }
     TO *Cp = static_cast<TO *>(p.c) + (DIR == DW ? wbase : 0);
+    if (T == 32) Cp += part * (DIR == DW ? (int64_t)p.G * p.n * p.k : p.rows * cols);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int r = at(ty, i);

@@ -68,6 +68,7 @@ moe_status simt_tiles(const simt::Args &a, cudaStream_t s) {
     const int64_t ct = (cols + t - 1) / t;
     return DIR == simt::DW ? (int64_t)a.G * ((a.n + t - 1) / t) * ct : (a.rows / t + a.G) * ct;
   };
+  if (a.splits > 1) return launch_simt<TI, TO, DIR, 32>(a, tiles(32) * a.splits, nsm, s);
   // the larger tile reuses each operand value more often; the smaller ones
   // where the larger would leave SMs without work
   if (tiles(128) >= 4 * nsm) return launch_simt<TI, TO, DIR, 128>(a, tiles(128), nsm, s);
@@ -110,6 +111,7 @@ simt::Args simt_args(const Product &p) {
   a.k = p.s->k;
   a.rows = p.s->rows;
   a.accumulate = p.accumulate;
+  a.splits = 1;
   a.status = p.status;
   return a;
 }
@@ -463,12 +465,32 @@ void split_dw_product(Plan &p, const moe_grouped_shape *s) {
   p.part = align_up((size_t)n * s->groups * s->n * s->k * 4, 256);
 }
 
+// The same on the CUDA cores, whose smallest tile is 32 x 32 and whose slices
+// are 64 deep (dx of two products, 6 groups, 5 rows, 1104 -> 64, fp32: 41 ->
+// 10 us).
+void split_simt_product(Plan &p, Kind kind, const moe_grouped_shape *s, int products) {
+  if (p.tensor()) return;
+  const int cols = kind == K_LINEAR ? s->n : s->k;
+  const int64_t contract = kind == K_LINEAR ? s->k : kind == K_DX ? s->n : mean_rows(s);
+  auto tiles = [&](int t) {
+    const int64_t ct = (cols + t - 1) / t;
+    return kind == K_DW ? (int64_t)s->groups * ((s->n + t - 1) / t) * ct : row_tiles(s, t) * ct;
+  };
+  if (tiles(64) >= SMS) return;  // enough of the larger ones
+  int64_t n = std::min<int64_t>({16, 2 * SMS / std::max<int64_t>(1, tiles(32)),
+                                 (contract + 63) / 64 * products / 3});
+  if (n < 3) return;
+  p.splits = (int)n;
+  p.part = align_up((size_t)n * 4 * (kind == K_DW ? (size_t)s->groups * s->n * s->k : (size_t)s->rows * cols), 256);
+}
+
 Plan plan_product(Kind kind, const moe_grouped_shape *s, const Operand *o, int n, moe_dtype dt,
                   int products, bool aligned) {
   Plan p = plan(kind, o, n, dt, flops_of(s, products), aligned);
   if (kind == K_LINEAR) split_rows_product(p, s, s->n, s->k, products);
   if (kind == K_DX) split_rows_product(p, s, s->k, s->n, products);
   if (kind == K_DW) split_dw_product(p, s);
+  split_simt_product(p, kind, s, products);
   return p;
 }
 
@@ -497,6 +519,19 @@ moe_status join(const Plan &pl, const Product &p, int64_t rows, int64_t cols, co
   return launch_status();
 }
 
+// On the CUDA cores, in parts if the plan says so.
+template <int DIR>
+moe_status run_simt(const Plan &pl, const Product &p, int64_t rows, int64_t cols,
+                    const int32_t *offsets) {
+  simt::Args a = simt_args(p);
+  if (pl.splits == 1) return simt_product<DIR>(a, p.dt, p.out_dt, p.stream);
+  a.splits = pl.splits;
+  a.c = static_cast<uint8_t *>(p.ws) + pl.bytes;
+  a.accumulate = 0;
+  const moe_status st = simt_product<DIR>(a, p.dt, MOE_F32, p.stream);
+  return st != MOE_OK ? st : join(pl, p, rows, cols, offsets);
+}
+
 template <int OP>
 moe_status run_rows(const Plan &pl, const Product &p, RowJob &j) {
   j.p.offsets = p.offsets;
@@ -515,7 +550,7 @@ moe_status run_linear(const Product &p) {
   Operand o[4];
   const int n = linear_ops(p.s, p.a0, p.b0, o);
   const Plan pl = plan_call(K_LINEAR, p.s, o, n, p.dt, 1, p.ws, p.ws_bytes);
-  if (!pl.tensor()) return simt_product<simt::LIN>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (!pl.tensor()) return run_simt<simt::LIN>(pl, p, p.s->rows, p.s->n, p.offsets);
   if (pl.staged) {
     const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
     if (st != MOE_OK) return st;
@@ -529,7 +564,7 @@ moe_status run_dx(const Product &p) {
   const bool two = p.a1 != nullptr;
   const int n = dx_ops(p.s, p.a0, p.b0, p.a1, p.b1, two, o);
   const Plan pl = plan_call(K_DX, p.s, o, n, p.dt, two ? 2 : 1, p.ws, p.ws_bytes);
-  if (!pl.tensor()) return simt_product<simt::DX>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (!pl.tensor()) return run_simt<simt::DX>(pl, p, p.s->rows, p.s->k, p.offsets);
   if (pl.staged) {
     const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
     if (st != MOE_OK) return st;
@@ -543,8 +578,8 @@ moe_status run_dw(const Product &p) {
   const int n = dw_ops(p.s, p.a0, p.b0, o);
   const Plan pl = plan_call(K_DW, p.s, o, n, p.dt, 1, p.ws, p.ws_bytes);
   // without rows there is nothing to map; the CUDA-core kernel writes the zeros
-  if (!pl.tensor() || p.s->rows == 0)
-    return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (p.s->rows == 0) return simt_product<simt::DW>(simt_args(p), p.dt, p.out_dt, p.stream);
+  if (!pl.tensor()) return run_simt<simt::DW>(pl, p, (int64_t)p.s->groups * p.s->n, p.s->k, nullptr);
   if (pl.staged) {
     const moe_status st = stage(o, n, p.dt, p.ws, p.stream);
     if (st != MOE_OK) return st;
@@ -693,13 +728,20 @@ MOE_EXPORT moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps
   return launch_status();
 }
 
+// A single product on the CUDA cores.
+static Plan cores_plan(Kind kind, const moe_grouped_shape *s) {
+  Plan p;
+  split_simt_product(p, kind, s, 1);
+  return p;
+}
+
 MOE_EXPORT size_t moe_swiglu_checkpoint_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
                                                        int32_t aligned) {
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
   const Plan p = plan(K_UP, o, up_ops(s, nullptr, nullptr, nullptr, o), dt, flops_of(s, 2), aligned);
-  // on the CUDA cores: the two projections in fp32
-  return p.tensor() ? p.bytes : 2 * align_up((size_t)s->rows * s->n * 4, 256);
+  // on the CUDA cores: the two projections in fp32, and what their product takes
+  return p.tensor() ? p.bytes : 2 * align_up((size_t)s->rows * s->n * 4, 256) + cores_plan(K_LINEAR, s).part;
 }
 
 MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const void *x,
@@ -732,12 +774,15 @@ MOE_EXPORT moe_status moe_swiglu_checkpoint(const moe_grouped_shape *s, const vo
     j.p.vec = s->n % 4 == 0 && aligned(h, 4 * elem(dt)) && aligned(codes_a, 4) && aligned(codes_u, 4);
     return dt == MOE_F32 ? tc_up<float>(j) : tc_up<bf16>(j);
   }
+  const size_t plane = align_up((size_t)s->rows * s->n * 4, 256);
   float *a = static_cast<float *>(ws);
-  float *u = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + align_up((size_t)s->rows * s->n * 4, 256));
-  if ((st = run_linear({s, dt, MOE_F32, x, w1, nullptr, nullptr, offsets, a, 0, nullptr, 0, dev_status, cs})) != MOE_OK)
-    return st;
-  if ((st = run_linear({s, dt, MOE_F32, x, w3, nullptr, nullptr, offsets, u, 0, nullptr, 0, dev_status, cs})) != MOE_OK)
-    return st;
+  float *u = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plane);
+  const Plan cores = cores_plan(K_LINEAR, s);
+  Product lin{s, dt, MOE_F32, x, w1, nullptr, nullptr, offsets, a, 0, u + plane / 4, cores.part, dev_status, cs};
+  if ((st = run_simt<simt::LIN>(cores, lin, s->rows, s->n, offsets)) != MOE_OK) return st;
+  lin.b0 = w3;
+  lin.out = u;
+  if ((st = run_simt<simt::LIN>(cores, lin, s->rows, s->n, offsets)) != MOE_OK) return st;
   const unsigned grid = row_grid(s->rows * scale_blocks(s->n));
   if (dt == MOE_F32)
     ckpt::swiglu_save<<<grid, ckpt::ROW_THREADS, 0, cs>>>(a, u, offsets, s->groups, s->rows, s->n, static_cast<float *>(h), sv);
@@ -756,7 +801,10 @@ MOE_EXPORT size_t moe_swiglu_backward_workspace_size(const moe_grouped_shape *s,
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
   const Plan p = plan(K_BWD, o, bwd_ops(s, nullptr, nullptr, o), dt, flops_of(s, 1), aligned);
-  return p.tensor() ? part_bytes(s) + p.bytes : (size_t)s->rows * s->n * 4;  // else dh in fp32
+  if (p.tensor()) return part_bytes(s) + p.bytes;
+  // dh in fp32, and what its product takes
+  const moe_grouped_shape lin{s->groups, s->k, s->n, s->rows};
+  return align_up((size_t)s->rows * s->n * 4, 256) + cores_plan(K_DX, &lin).part;
 }
 
 MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void *dy, moe_dtype dt,
@@ -802,11 +850,14 @@ MOE_EXPORT moe_status moe_swiglu_backward(const moe_grouped_shape *s, const void
         j.p.part, offsets, s->groups, s->rows, scale_blocks(s->n), dgate);
     return launch_status();
   }
+  const size_t plane = align_up((size_t)s->rows * s->n * 4, 256);
   float *dh = static_cast<float *>(ws);
   // dh = dy w2: the input gradient of a linear layer from n features to k
   const moe_grouped_shape lin{s->groups, s->k, s->n, s->rows};
-  if ((st = run_dx({&lin, dt, MOE_F32, dy, w2, nullptr, nullptr, offsets, dh, 0, nullptr, 0, dev_status, cs})) != MOE_OK)
-    return st;
+  const Plan cores = cores_plan(K_DX, &lin);
+  const Product q{&lin, dt, MOE_F32, dy, w2, nullptr, nullptr, offsets, dh, 0, static_cast<uint8_t *>(ws) + plane,
+                  cores.part, dev_status, cs};
+  if ((st = run_simt<simt::DX>(cores, q, s->rows, s->n, offsets)) != MOE_OK) return st;
   const unsigned grid = row_grid(s->rows * (ckpt::ROW_THREADS / 32));
   if (dt == MOE_F32)
     ckpt::swiglu_grads<<<grid, ckpt::ROW_THREADS, 0, cs>>>(
