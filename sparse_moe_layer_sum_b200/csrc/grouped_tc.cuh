@@ -557,120 +557,120 @@ __global__ void __launch_bounds__(RowCfg<OP, CG, AT, BN, STAGES, SEGS>::NT, 1)
 
   if (warp < 4) {
     if (C::EPI == 8) regs_low();
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------ TMA producer
-      // a weight tile that several row tiles of its group read is kept in L2,
-      // one that is read once leaves first; the rows are read by every
-      // feature tile
-      const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
-      const uint64_t pol_b = policy_evict_last();
-      Ring r;
-      bool ok = true;
-      for (int tile = unit; ok && tile < total; tile += nunits) {
-        const Tile t = find_tile(tab, whole(tile), p.G);
-        const int nkb = blocks(tile);
-        const uint64_t pol_a = t.ntt > 1 ? keep : once;
-        const int brows = ((t.nvalid + 15) & ~15) / CG;  // this SM's share
-        const int b0 = t.row0 + (int)rank * brows;
-        const int f0 = t.ft * C::FEAT + (int)rank * BM;
-        const int nbox = (brows + C::BOXN - 1) / C::BOXN;
-        const uint32_t bytes = (uint32_t)(C::A_ALL + nbox * C::BOXN * BK * 2);
-        // tiles that run together start at different k-blocks, which spreads
-        // their reads of shared operands over L2
-        const int k0 = splits == 1 ? (t.ft * 7 + t.tt * 5) % p.kb : part_of(tile) * per;
-        int q = k0 / p.kb0, blk = k0 - q * p.kb0;  // pass (of all sources) and block of it
-        for (int i = 0; i < nkb; ++i) {
-          if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
-            ok = false;
-            break;
-          }
-          // the leader's barrier counts the bytes of both SMs
-          if (leader) mbar_arrive_expect_tx(full + r.stage, bytes * CG);
-          pending[r.stage] = (int)r.phase;
-          uint8_t *a = sm + r.stage * C::STAGE, *b = a + C::A_ALL;
-          const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(full + r.stage), 0) : smem_u32(full + r.stage);
-          const bool second = q >= p.passes;
-          const int kk = blk * BK;
-          const int term = p.passes == 1 ? SPLIT_PASSES - 1 : second ? q - p.passes : q;
-          const int za = term_a(term) * p.G + t.g;                    // plane of the weights
-          const int yb = term_b(term) * (int)p.rows + b0;             // row of the row planes
-          if (++blk == p.kb0) {
-            blk = 0;
-            if (++q * p.kb0 == p.kb) q = 0;
-          }
-          const CUtensorMap *ma = second ? &tmA1 : &tmA0, *mb = second ? &tmB1 : &tmB0;
-#pragma unroll
-          for (int i2 = 0; i2 < AT; ++i2) {
-            const int f = f0 + (OP == UP ? 0 : i2 * BM * CG);
-            if (C::KMAJOR) {
-              load_3d<CG>(OP == UP && i2 == 1 ? &tmA1 : ma, a + i2 * TILE, bar, kk, f, za, pol_a);
-            } else {
-              load_3d<CG>(ma, a + i2 * TILE, bar, f, kk, za, pol_a);
-              load_3d<CG>(ma, a + i2 * TILE + BOX, bar, f + 64, kk, za, pol_a);
+    if (warp == 0) {
+      if (lane == 0) {
+        // ------------------------------------------------------ TMA producer
+        // a weight tile that several row tiles of its group read is kept in L2,
+        // one that is read once leaves first; the rows are read by every
+        // feature tile
+        const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
+        const uint64_t pol_b = policy_evict_last();
+        Ring r;
+        bool ok = true;
+        for (int tile = unit; ok && tile < total; tile += nunits) {
+          const Tile t = find_tile(tab, whole(tile), p.G);
+          const int nkb = blocks(tile);
+          const uint64_t pol_a = t.ntt > 1 ? keep : once;
+          const int brows = ((t.nvalid + 15) & ~15) / CG;  // this SM's share
+          const int b0 = t.row0 + (int)rank * brows;
+          const int f0 = t.ft * C::FEAT + (int)rank * BM;
+          const int nbox = (brows + C::BOXN - 1) / C::BOXN;
+          const uint32_t bytes = (uint32_t)(C::A_ALL + nbox * C::BOXN * BK * 2);
+          // tiles that run together start at different k-blocks, which spreads
+          // their reads of shared operands over L2
+          const int k0 = splits == 1 ? (t.ft * 7 + t.tt * 5) % p.kb : part_of(tile) * per;
+          int q = k0 / p.kb0, blk = k0 - q * p.kb0;  // pass (of all sources) and block of it
+          for (int i = 0; i < nkb; ++i) {
+            if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
+              ok = false;
+              break;
             }
+            // the leader's barrier counts the bytes of both SMs
+            if (leader) mbar_arrive_expect_tx(full + r.stage, bytes * CG);
+            pending[r.stage] = (int)r.phase;
+            uint8_t *a = sm + r.stage * C::STAGE, *b = a + C::A_ALL;
+            const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(full + r.stage), 0) : smem_u32(full + r.stage);
+            const bool second = q >= p.passes;
+            const int kk = blk * BK;
+            const int term = p.passes == 1 ? SPLIT_PASSES - 1 : second ? q - p.passes : q;
+            const int za = term_a(term) * p.G + t.g;                    // plane of the weights
+            const int yb = term_b(term) * (int)p.rows + b0;             // row of the row planes
+            if (++blk == p.kb0) {
+              blk = 0;
+              if (++q * p.kb0 == p.kb) q = 0;
+            }
+            const CUtensorMap *ma = second ? &tmA1 : &tmA0, *mb = second ? &tmB1 : &tmB0;
+#pragma unroll
+            for (int i2 = 0; i2 < AT; ++i2) {
+              const int f = f0 + (OP == UP ? 0 : i2 * BM * CG);
+              if (C::KMAJOR) {
+                load_3d<CG>(OP == UP && i2 == 1 ? &tmA1 : ma, a + i2 * TILE, bar, kk, f, za, pol_a);
+              } else {
+                load_3d<CG>(ma, a + i2 * TILE, bar, f, kk, za, pol_a);
+                load_3d<CG>(ma, a + i2 * TILE + BOX, bar, f + 64, kk, za, pol_a);
+              }
+            }
+            for (int j = 0; j < nbox; ++j)
+              load_2d<CG>(mb, b + j * C::BOXN * BK * 2, bar, kk, yb + j * C::BOXN, pol_b);
+            r.next(STAGES);
           }
-          for (int j = 0; j < nbox; ++j)
-            load_2d<CG>(mb, b + j * C::BOXN * BK * 2, bar, kk, yb + j * C::BOXN, pol_b);
-          r.next(STAGES);
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0 && leader) {
+        // -------------------------------------------------------- MMA issuer
+        Ring r, acc;
+        bool ok = true;
+        for (int tile = unit; ok && tile < total; tile += nunits) {
+          const Tile t = find_tile(tab, whole(tile), p.G);
+          const int nkb = blocks(tile);
+          const uint32_t idesc =
+              idesc_bf16_f32(BM * CG, (t.nvalid + 15) & ~15) | (C::KMAJOR ? 0u : A_MN);
+          uint32_t d = 0;
+          int seg = 0, cut = 0;  // segments begun, the k-block that begins the next
+          for (int kb = 0; kb < nkb; ++kb) {
+            const bool first = SEGS ? kb == cut : kb == 0;
+            if (first) {
+              if (SEGS) cut += segment<OP>(seg++, nkb);
+              if (kb > 0) {
+                commit<CG>(accf + acc.stage);
+                acc.next(C::NBUF);
+              }
+              if (!(ok = wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status))) break;
+              d = tmem + (uint32_t)(acc.stage * C::ACC);
+            }
+            if (!(ok = wait_bounded(full + r.stage, r.phase, abort_flag, WAIT_NS, p.status))) break;
+            pending[r.stage] = -1;
+            tc_fence_after();
+            const uint32_t a = smem_u32(sm + r.stage * C::STAGE), b = a + C::A_ALL;
+            // MMAs that share their rows back to back: the other order, all of
+            // one A tile first, was 5% slower
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              const uint64_t bd = sdesc_sw128(b + kk * 32);
+#pragma unroll
+              for (int i = 0; i < AT; ++i) {
+                const uint64_t ad = C::KMAJOR ? sdesc_sw128(a + i * TILE + kk * 32)
+                                              : desc_mn(a + i * TILE + kk * 2048);
+                mma<CG>(d + i * BN, ad, bd, idesc, first && kk == 0 ? 0u : 1u);
+              }
+            }
+            commit<CG>(empty + r.stage);
+            r.next(STAGES);
+          }
+          if (!ok) break;
+          commit<CG>(accf + acc.stage);
+          acc.next(C::NBUF);
+        }
+        if (!ok) {  // no MMA may still write tensor memory when it is freed
+          if (CG == 2)
+            mma_commit_pair(drained);
+          else
+            mma_commit(drained);
+          drain(drained, 0);
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // -------------------------------------------------------- MMA issuer
-      Ring r, acc;
-      bool ok = true;
-      for (int tile = unit; ok && tile < total; tile += nunits) {
-        const Tile t = find_tile(tab, whole(tile), p.G);
-        const int nkb = blocks(tile);
-        const uint32_t idesc =
-            idesc_bf16_f32(BM * CG, (t.nvalid + 15) & ~15) | (C::KMAJOR ? 0u : A_MN);
-        uint32_t d = 0;
-        int seg = 0, cut = 0;  // segments begun, the k-block that begins the next
-        for (int kb = 0; kb < nkb; ++kb) {
-          const bool first = SEGS ? kb == cut : kb == 0;
-          if (first) {
-            if (SEGS) cut += segment<OP>(seg++, nkb);
-            if (kb > 0) {
-              commit<CG>(accf + acc.stage);
-              acc.next(C::NBUF);
-            }
-            if (!(ok = wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status))) break;
-            d = tmem + (uint32_t)(acc.stage * C::ACC);
-          }
-          if (!(ok = wait_bounded(full + r.stage, r.phase, abort_flag, WAIT_NS, p.status))) break;
-          pending[r.stage] = -1;
-          tc_fence_after();
-          const uint32_t a = smem_u32(sm + r.stage * C::STAGE), b = a + C::A_ALL;
-          // MMAs that share their rows back to back: the other order, all of
-          // one A tile first, was 5% slower
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t bd = sdesc_sw128(b + kk * 32);
-#pragma unroll
-            for (int i = 0; i < AT; ++i) {
-              const uint64_t ad = C::KMAJOR ? sdesc_sw128(a + i * TILE + kk * 32)
-                                            : desc_mn(a + i * TILE + kk * 2048);
-              mma<CG>(d + i * BN, ad, bd, idesc, first && kk == 0 ? 0u : 1u);
-            }
-          }
-          commit<CG>(empty + r.stage);
-          r.next(STAGES);
-        }
-        if (!ok) break;
-        commit<CG>(accf + acc.stage);
-        acc.next(C::NBUF);
-      }
-      if (!ok) {  // no MMA may still write tensor memory when it is freed
-        if (CG == 2)
-          mma_commit_pair(drained);
-        else
-          mma_commit(drained);
-        drain(drained, 0);
-      }
-    }
-  }
   } else {
     if (C::EPI == 8) regs_high();
     // -------------------------------------------------------------- epilogue
@@ -971,128 +971,128 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
 
   if (warp < 4) {
     regs_low();
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------ TMA producer
-      const uint64_t pol = policy_evict_normal();
+    if (warp == 0) {
+      if (lane == 0) {
+        // ------------------------------------------------------ TMA producer
+        const uint64_t pol = policy_evict_normal();
+        Ring r;
+        bool ok = true;
+        for (int64_t tile = unit; ok && tile < total; tile += nunits) {
+          const Job j = job(tile);
+          const int hb = j.nmma / 2, nbox = (hb + 63) / 64;
+          const int n0 = j.n0 + (int)rank * BM, k0 = j.k0 + (int)rank * hb;
+          const uint32_t bytes = (uint32_t)(AT * TILE + nbox * BOX);
+          int q = 0, blk = 0;  // pass and block of it
+          for (int i = 0; i < j.kb; ++i) {
+            if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
+              ok = false;
+              break;
+            }
+            // a last block that ends inside a 16-row step is completed on each
+            // SM's own `tail` barrier and handed on when its rows are zeroed
+            const bool fix = j.fix(blk);
+            uint32_t bar;
+            if (fix) {
+              mbar_arrive_expect_tx(tail + r.stage, bytes);
+              bar = mapa_shared(smem_u32(tail + r.stage), rank);
+            } else {
+              mbar_arrive(tail + r.stage);
+              if (leader) {
+                mbar_arrive_expect_tx(full + r.stage, bytes * 2);
+                mbar_arrive(full + r.stage);
+              }
+              bar = mapa_shared(smem_u32(full + r.stage), 0);
+            }
+            pending[r.stage] = (int)r.phase + (fix ? 2 : 0);
+            uint8_t *a = sm + r.stage * C::STAGE, *b = a + AT * TILE;
+            const int term = p.passes == 1 ? SPLIT_PASSES - 1 : q;
+            const int row = j.lo + blk * BK;
+            const int ya = term_a(term) * (int)p.rows + row, yb = term_b(term) * (int)p.rows + row;
+            if (++blk == j.kb0) {
+              blk = 0;
+              ++q;
+            }
+#pragma unroll
+            for (int c = 0; c < 2 * AT; ++c)
+              load_2d<2>(&tmA, a + c * BOX, bar, n0 + c / 2 * 256 + c % 2 * 64, ya, pol);
+            for (int c = 0; c < nbox; ++c) load_2d<2>(&tmB, b + c * BOX, bar, k0 + c * 64, yb, pol);
+            r.next(STAGES);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0 && leader) {
+        // -------------------------------------------------------- MMA issuer
+        Ring r, acc;
+        bool ok = true;
+        for (int64_t tile = unit; ok && tile < total; tile += nunits) {
+          const Job j = job(tile);
+          if (j.kb == 0) continue;
+          const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
+          uint32_t d = 0;
+          for (int i = 0, blk = 0; i < j.kb; ++i, blk = blk + 1 == j.kb0 ? 0 : blk + 1) {
+            const bool first = i == 0 || (C::SEGS && i % SEG == 0);
+            if (first) {
+              if (i > 0) {
+                commit<2>(accf + acc.stage);
+                acc.next(C::NBUF);
+              }
+              if (!(ok = wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status))) break;
+              d = tmem + (uint32_t)(acc.stage * AT * 256);
+            }
+            if (!(ok = wait_bounded(full + r.stage, r.phase, abort_flag, WAIT_NS, p.status))) break;
+            pending[r.stage] = -1;
+            tc_fence_after();
+            const uint32_t a = smem_u32(sm + r.stage * C::STAGE), b = a + AT * TILE;
+            const int steps = (j.depth(blk) + 15) / 16;
+            for (int s = 0; s < steps; ++s)
+#pragma unroll
+              for (int c = 0; c < AT; ++c)
+                mma<2>(d + c * 256, desc_mn(a + c * TILE + s * 2048), desc_mn(b + s * 2048), idesc,
+                       first && s == 0 ? 0u : 1u);
+            commit<2>(empty + r.stage);
+            r.next(STAGES);
+          }
+          if (!ok) break;
+          commit<2>(accf + acc.stage);
+          acc.next(C::NBUF);
+        }
+        if (!ok) {
+          mma_commit_pair(drained);
+          drain(drained, 0);
+        }
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------- tail rows, ahead of the MMAs
+      // (done by the issuing warp itself, this held up every tile of a short
+      // group: 455 -> 385 us for 32 groups of about 128 rows)
       Ring r;
-      bool ok = true;
-      for (int64_t tile = unit; ok && tile < total; tile += nunits) {
+      for (int64_t tile = unit; tile < total; tile += nunits) {
         const Job j = job(tile);
-        const int hb = j.nmma / 2, nbox = (hb + 63) / 64;
-        const int n0 = j.n0 + (int)rank * BM, k0 = j.k0 + (int)rank * hb;
-        const uint32_t bytes = (uint32_t)(AT * TILE + nbox * BOX);
-        int q = 0, blk = 0;  // pass and block of it
-        for (int i = 0; i < j.kb; ++i) {
-          if (!wait_bounded(empty + r.stage, r.phase ^ 1u, abort_flag, WAIT_NS, p.status)) {
-            ok = false;
+        for (int i = 0, blk = 0; i < j.kb; ++i, blk = blk + 1 == j.kb0 ? 0 : blk + 1) {
+          if (!wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
+            tile = total;
             break;
           }
-          // a last block that ends inside a 16-row step is completed on each
-          // SM's own `tail` barrier and handed on when its rows are zeroed
-          const bool fix = j.fix(blk);
-          uint32_t bar;
-          if (fix) {
-            mbar_arrive_expect_tx(tail + r.stage, bytes);
-            bar = mapa_shared(smem_u32(tail + r.stage), rank);
-          } else {
-            mbar_arrive(tail + r.stage);
-            if (leader) {
-              mbar_arrive_expect_tx(full + r.stage, bytes * 2);
-              mbar_arrive(full + r.stage);
+          if (j.fix(blk)) {
+            // rows tail .. next multiple of 16 of every 64-column box: 128
+            // bytes each, whole rows, so the swizzle does not matter
+            uint8_t *st = sm + r.stage * C::STAGE + j.tail * 128;
+            const int bytes = (16 - j.tail % 16) * 128, nbox = 2 * AT + (j.nmma / 2 + 63) / 64;
+            for (int bx = 0; bx < nbox; ++bx)
+              for (int at = lane * 16; at < bytes; at += 512)
+                *reinterpret_cast<uint4 *>(st + bx * BOX + at) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              pending[r.stage] = -1;
+              arrive_cluster(mapa_shared(smem_u32(full + r.stage), 0));
             }
-            bar = mapa_shared(smem_u32(full + r.stage), 0);
           }
-          pending[r.stage] = (int)r.phase + (fix ? 2 : 0);
-          uint8_t *a = sm + r.stage * C::STAGE, *b = a + AT * TILE;
-          const int term = p.passes == 1 ? SPLIT_PASSES - 1 : q;
-          const int row = j.lo + blk * BK;
-          const int ya = term_a(term) * (int)p.rows + row, yb = term_b(term) * (int)p.rows + row;
-          if (++blk == j.kb0) {
-            blk = 0;
-            ++q;
-          }
-#pragma unroll
-          for (int c = 0; c < 2 * AT; ++c)
-            load_2d<2>(&tmA, a + c * BOX, bar, n0 + c / 2 * 256 + c % 2 * 64, ya, pol);
-          for (int c = 0; c < nbox; ++c) load_2d<2>(&tmB, b + c * BOX, bar, k0 + c * 64, yb, pol);
           r.next(STAGES);
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // -------------------------------------------------------- MMA issuer
-      Ring r, acc;
-      bool ok = true;
-      for (int64_t tile = unit; ok && tile < total; tile += nunits) {
-        const Job j = job(tile);
-        if (j.kb == 0) continue;
-        const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
-        uint32_t d = 0;
-        for (int i = 0, blk = 0; i < j.kb; ++i, blk = blk + 1 == j.kb0 ? 0 : blk + 1) {
-          const bool first = i == 0 || (C::SEGS && i % SEG == 0);
-          if (first) {
-            if (i > 0) {
-              commit<2>(accf + acc.stage);
-              acc.next(C::NBUF);
-            }
-            if (!(ok = wait_bounded(acce + acc.stage, acc.phase ^ 1u, abort_flag, WAIT_NS, p.status))) break;
-            d = tmem + (uint32_t)(acc.stage * AT * 256);
-          }
-          if (!(ok = wait_bounded(full + r.stage, r.phase, abort_flag, WAIT_NS, p.status))) break;
-          pending[r.stage] = -1;
-          tc_fence_after();
-          const uint32_t a = smem_u32(sm + r.stage * C::STAGE), b = a + AT * TILE;
-          const int steps = (j.depth(blk) + 15) / 16;
-          for (int s = 0; s < steps; ++s)
-#pragma unroll
-            for (int c = 0; c < AT; ++c)
-              mma<2>(d + c * 256, desc_mn(a + c * TILE + s * 2048), desc_mn(b + s * 2048), idesc,
-                     first && s == 0 ? 0u : 1u);
-          commit<2>(empty + r.stage);
-          r.next(STAGES);
-        }
-        if (!ok) break;
-        commit<2>(accf + acc.stage);
-        acc.next(C::NBUF);
-      }
-      if (!ok) {
-        mma_commit_pair(drained);
-        drain(drained, 0);
-      }
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------- tail rows, ahead of the MMAs
-    // (done by the issuing warp itself, this held up every tile of a short
-    // group: 455 -> 385 us for 32 groups of about 128 rows)
-    Ring r;
-    for (int64_t tile = unit; tile < total; tile += nunits) {
-      const Job j = job(tile);
-      for (int i = 0, blk = 0; i < j.kb; ++i, blk = blk + 1 == j.kb0 ? 0 : blk + 1) {
-        if (!wait_warp(tail + r.stage, r.phase, abort_flag, p.status)) {
-          tile = total;
-          break;
-        }
-        if (j.fix(blk)) {
-          // rows tail .. next multiple of 16 of every 64-column box: 128
-          // bytes each, whole rows, so the swizzle does not matter
-          uint8_t *st = sm + r.stage * C::STAGE + j.tail * 128;
-          const int bytes = (16 - j.tail % 16) * 128, nbox = 2 * AT + (j.nmma / 2 + 63) / 64;
-          for (int bx = 0; bx < nbox; ++bx)
-            for (int at = lane * 16; at < bytes; at += 512)
-              *reinterpret_cast<uint4 *>(st + bx * BOX + at) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            pending[r.stage] = -1;
-            arrive_cluster(mapa_shared(smem_u32(full + r.stage), 0));
-          }
-        }
-        r.next(STAGES);
-      }
-    }
-  }
   } else {
     regs_high();
     // -------------------------------------------------------------- epilogue
