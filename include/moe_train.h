@@ -79,7 +79,8 @@ moe_status moe_grouped_linear_dx(const moe_grouped_shape *s, const void *dy, moe
  * dy[p,:]^T x[p,:], added to dw when accumulate is 1.
  *   dy [rows, n], x [rows, k] of type dt; dw [groups, n, k] of type dw_dt
  * A group without rows has a zero gradient (accumulate 0) or leaves its part
- * of dw as it was (accumulate 1).
+ * of dw as it was (accumulate 1).  The addition to dw is one more rounding of
+ * the sum in fp32 (fp32 sums below 2^-126 may become zero in it).
  */
 size_t moe_grouped_linear_dw_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
                                             int32_t aligned);

@@ -85,6 +85,14 @@ __device__ __forceinline__ void store_3d(const CUtensorMap *m, const void *src, 
                "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
                : "memory");
 }
+// The same, added to what is there (fp32, one rounding; the memory system
+// flushes subnormal sums to zero).
+__device__ __forceinline__ void reduce_3d(const CUtensorMap *m, const void *src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void store_wait_read() {
@@ -1099,6 +1107,8 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     const int q = warp & 3, half = (warp - 4) >> 2;
     constexpr int CH = C::CHUNK, NCH = 128 / CH;  // this warp's 128 columns in chunks
     uint8_t *stg = sm + C::STG + (warp - 4) * 4096;
+    // fp32 sums are added to dw by the copy itself (an element has one tile)
+    const bool reduce = sizeof(TO) == 4 && p.accumulate && p.tma_store;
     Ring acc;
     uint32_t tb = 0;
     auto acquire = [&]() {
@@ -1129,7 +1139,10 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            store_3d(&tmC, stg, k0, n0, j.g);
+            if (reduce)
+              reduce_3d(&tmC, stg, k0, n0, j.g);
+            else
+              store_3d(&tmC, stg, k0, n0, j.g);
             store_commit();
           }
           return;
@@ -1148,11 +1161,42 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
       auto emit = [&](float (&v)[CH], int c) {
         const int n0 = j.n0 + (int)rank * BM + q * 32, k0 = j.k0 + half * 128 + c * CH;
         if (k0 >= p.k || n0 >= p.n) return;
-        if (p.accumulate && n0 + lane < p.n) {
-          const TO *o = static_cast<const TO *>(p.dw) + ((size_t)j.g * p.n + n0 + lane) * p.k + k0;
+        if (p.accumulate && !reduce) {
+          if (sizeof(TO) == 2 && p.tma_store) {
+            // old values: whole rows of the chunk (8 lanes of 16 bytes each)
+            // into the staging buffer, from there each lane's own row
+            const TO *o = static_cast<const TO *>(p.dw) + ((size_t)j.g * p.n + n0) * p.k + k0;
+            uint4 old[8];
 #pragma unroll
-          for (int i = 0; i < CH; ++i)
-            if (k0 + i < p.k) v[i] += to_f(o[i]);
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + lane / 8, u = lane % 8 * 8;
+              old[i] = make_uint4(0, 0, 0, 0);
+              if (n0 + r < p.n && k0 + u < p.k) old[i] = *reinterpret_cast<const uint4 *>(o + (size_t)r * p.k + u);
+            }
+            if (lane == 0) store_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + lane / 8;
+              *reinterpret_cast<uint4 *>(stg + r * 128 + (((lane % 8) ^ (r & 7)) << 4)) = old[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(stg + lane * 128 + ((i ^ (lane & 7)) << 4));
+              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                v[(8 * i + 2 * e) % CH] += __uint_as_float(x[e] << 16);
+                v[(8 * i + 2 * e + 1) % CH] += __uint_as_float(x[e] & 0xffff0000u);
+              }
+            }
+          } else if (n0 + lane < p.n) {
+            const TO *o = static_cast<const TO *>(p.dw) + ((size_t)j.g * p.n + n0 + lane) * p.k + k0;
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              if (k0 + i < p.k) v[i] += to_f(o[i]);
+          }
         }
         store(n0, k0, [&](int i) {
           if (sizeof(TO) == 4) return __float_as_uint(v[i % CH]);

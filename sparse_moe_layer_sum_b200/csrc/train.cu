@@ -256,7 +256,10 @@ Plan plan(Kind kind, const Operand *ops, int n, moe_dtype dt, double flops, bool
   bool fits = dt == MOE_BF16;
   for (int i = 0; i < n; ++i) {
     fits = fits && aligned && ops[i].cols % 8 == 0;
-    if (ops[i].rows * p.terms >= ((int64_t)1 << 31)) return p;  // 32-bit row coordinates
+    if (ops[i].rows * p.terms >= ((int64_t)1 << 31)) {  // row coordinates are 32-bit
+      p.bytes = 0;
+      return p;
+    }
     p.bytes += align_up((size_t)ops[i].rows * padded(ops[i].cols) * p.terms * 2, 256);
   }
   if (fits) {

@@ -111,6 +111,8 @@ def test_workspaces():
     assert size("swiglu_backward", s, BF16, 1) >= 10 * 2 * 4     # a term for 32 features of a row
     for name in ("grouped_linear", "grouped_linear_dw", "swiglu_checkpoint", "swiglu_backward"):
         assert size(name, shape(groups=0), BF16, 1) == size(name, s, E4M3, 1) == 0
+    # three terms of so many rows are past 32-bit coordinates: nothing is copied
+    assert size("grouped_linear", shape(rows=1 << 30, n=8, k=8), F32, 1) == 0
     # too small or off its alignment
     assert back(s, nws=16) == WORKSPACE and back(s, ws=None) == WORKSPACE
     assert back(s, ws=ctypes.c_void_p(0x1004)) == WORKSPACE
