@@ -16,7 +16,6 @@ namespace moe {
 namespace {
 
 using grouped::bf16;
-using grouped::Table;
 
 // SMs of a B200: what the choices that size a workspace go by, without asking
 // a device

@@ -483,6 +483,45 @@ def test_no_rows():
     assert moe.restore_rows(c).shape == (0, 64)
 
 
+def test_rows_that_belong_to_no_group():
+    """Rows, but only empty groups: nothing is written, and dw is zero."""
+    x, w = R.normal(1, 64, 128).cuda(), R.normal(2, 3, 96, 128).cuda()
+    y = torch.full((64, 96), 5.0, dtype=BF, device="cuda")
+    for at in (0, 7, 64):
+        o = offs([at] * 4)
+        assert moe.grouped_linear(x, w, o, out=y) is y and (y == 5).all()
+        assert (moe.grouped_linear_dw(y, x, o) == 0).all()
+        base = R.normal(3, 3, 96, 128, dtype=F32).cuda()
+        acc = base.clone()
+        moe.grouped_linear_dw(y, x, o, out=acc, accumulate=True)
+        assert torch.equal(acc, base)
+        h, a, u = moe.swiglu_checkpoint(x, w, w, o)
+        moe.swiglu_backward(x, w.transpose(1, 2).contiguous(), a, u, o)
+
+
+def test_calls_from_several_threads():
+    import threading
+    t = chain_inputs(60)
+    want = run_all(t)
+    torch.cuda.synchronize()
+    same = {}
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(10):
+                got = run_all(t)
+            s.synchronize()
+            same[i] = all(torch.equal(a, b) for a, b in zip(got, want))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert same == {0: True, 1: True, 2: True}
+
+
 def run_all(t):
     """Every operator once, chained as a backward pass would; results in a list."""
     h, a, u = moe.swiglu_checkpoint(t["x"], t["w1"], t["w3"], t["off"])
