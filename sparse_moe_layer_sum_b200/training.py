@@ -90,9 +90,10 @@ def _call(dev: int, sym: str, *args) -> None:
 
 
 def _groups(offsets: torch.Tensor) -> int:
-    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2,
-          "offsets must be int32 [groups + 1]")
-    return offsets.numel() - 1
+    n = offsets.shape
+    if offsets.dtype != torch.int32 or len(n) != 1 or n[0] < 2:
+        raise ValueError("offsets must be int32 [groups + 1]")
+    return n[0] - 1
 
 
 def _dtype(t: torch.Tensor, *others: torch.Tensor) -> int:
@@ -106,40 +107,50 @@ def _dtype(t: torch.Tensor, *others: torch.Tensor) -> int:
     return dt
 
 
-def _out(out, shape, dtype, dev: int) -> torch.Tensor:
-    if dtype not in _DT:
-        raise ValueError("outputs must be bf16 or fp32")
+def _out(out, out_dtype, dtype, dev: int, *shape: int):
+    """(`out` or a new tensor, its dtype code) for a result of `shape`, in
+    out_dtype or else `dtype`."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(tuple(out.shape) == tuple(shape) and out.dtype == dtype, "out has another shape or dtype")
-    return out
+        dtype = out_dtype or dtype
+    elif out.shape != shape or (out_dtype or out.dtype) != out.dtype:
+        raise ValueError("out has another shape or dtype")
+    else:
+        dtype = out.dtype
+    dt = _DT.get(dtype)
+    if dt is None:
+        raise ValueError("outputs must be bf16 or fp32")
+    return (torch.empty(*shape, dtype=dtype, device=dev) if out is None else out), dt
 
 
 def _status(status: Optional[torch.Tensor]) -> Optional[int]:
-    if status is not None:
-        _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32")
-    return _ptr(status)
+    if status is None:
+        return None
+    _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32")
+    return status.data_ptr()
 
 
-_bytes: dict = {}  # workspace sizes by what they depend on
+_plans: dict = {}  # (moe_grouped_shape, workspace bytes) by what they depend on
 
 
-def _workspace(sym: str, shape: MoEGroupedShape, dt: int, dev, operands, *flags: int):
-    """(tensor or None, address or None, bytes) of the workspace `sym` asks for."""
+def _plan(sym: str, dev: int, G: int, n: int, k: int, rows: int, dt: int, operands, *flags: int):
+    """(shape, workspace or None, its address or None, its bytes) for a call whose
+    workspace `sym` states; operands are the tensors its alignment goes by."""
     aligned = 1
     for t in operands:
         if t.data_ptr() & 15:
             aligned = 0
-    key = (sym, shape.groups, shape.n, shape.k, shape.rows, dt, aligned, *flags)
-    need = _bytes.get(key)
-    if need is None:
-        if len(_bytes) > 4096:
-            _bytes.clear()
-        need = _bytes[key] = _entry(sym)(ctypes.byref(shape), dt, *flags, aligned)
+    key = (sym, G, n, k, rows, dt, aligned, flags)
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) > 4096:
+            _plans.clear()
+        shape = ctypes.byref(MoEGroupedShape(G, n, k, rows))
+        p = _plans[key] = (shape, _entry(sym)(shape, dt, *flags, aligned))
+    shape, need = p
     if not need:
-        return None, None, 0
+        return shape, None, None, 0
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    return ws, ws.data_ptr(), need
+    return shape, ws, ws.data_ptr(), need
 
 
 def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
@@ -149,15 +160,15 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
     x [rows, k], w [groups, n, k] -> y [rows, n] (x's dtype unless out_dtype)."""
     dev = _check(x, w, offsets, out, status)
     G = _groups(offsets)
-    _need(x.dim() == 2 and w.dim() == 3 and w.shape[0] == G and w.shape[2] == x.shape[1],
-          "x must be [rows, k] and w [groups, n, k]")
+    xs, wsh = x.shape, w.shape
+    if len(xs) != 2 or len(wsh) != 3 or wsh[0] != G or wsh[2] != xs[1]:
+        raise ValueError("x must be [rows, k] and w [groups, n, k]")
     dt = _dtype(x, w)
-    rows, n = x.shape[0], w.shape[1]
-    out = _out(out, (rows, n), out_dtype or (x.dtype if out is None else out.dtype), dev)
-    shape = MoEGroupedShape(G, n, x.shape[1], rows)
-    ws, at, nws = _workspace("moe_grouped_linear_workspace_size", shape, dt, dev, (x, w))
-    _call(dev, "moe_grouped_linear", ctypes.byref(shape), x.data_ptr(), dt, w.data_ptr(),
-          offsets.data_ptr(), out.data_ptr(), _DT[out.dtype], at, nws, _status(status))
+    (rows, k), n = xs, wsh[1]
+    out, odt = _out(out, out_dtype, x.dtype, dev, rows, n)
+    shape, ws, at, nws = _plan("moe_grouped_linear_workspace_size", dev, G, n, k, rows, dt, (x, w))
+    _call(dev, "moe_grouped_linear", shape, x.data_ptr(), dt, w.data_ptr(), offsets.data_ptr(),
+          out.data_ptr(), odt, at, nws, _status(status))
     return out
 
 
@@ -169,22 +180,21 @@ def grouped_linear_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, 
     dy [rows, n], w [groups, n, k] -> dx [rows, k] (dy's dtype unless out_dtype)."""
     dev = _check(dy, w, dy2, w2, offsets, out, status)
     G = _groups(offsets)
-    _need(dy.dim() == 2 and w.dim() == 3 and w.shape[0] == G and w.shape[1] == dy.shape[1],
-          "dy must be [rows, n] and w [groups, n, k]")
-    _need((dy2 is None) == (w2 is None), "dy2 and w2 come together")
-    dt = _dtype(dy, w)
-    if dy2 is not None:
-        _need(dy2.shape == dy.shape and w2.shape == w.shape, "dy2 and w2 must match dy and w")
-        _dtype(dy, dy2, w2)
-    rows, k = dy.shape[0], w.shape[2]
-    out = _out(out, (rows, k), out_dtype or (dy.dtype if out is None else out.dtype), dev)
-    shape = MoEGroupedShape(G, w.shape[1], k, rows)
+    ys, wsh = dy.shape, w.shape
+    if len(ys) != 2 or len(wsh) != 3 or wsh[0] != G or wsh[1] != ys[1]:
+        raise ValueError("dy must be [rows, n] and w [groups, n, k]")
     two = dy2 is not None
-    ws, at, nws = _workspace("moe_grouped_linear_dx_workspace_size", shape, dt, dev,
-                             (dy, w, dy2, w2) if two else (dy, w), int(two))
-    _call(dev, "moe_grouped_linear_dx", ctypes.byref(shape), dy.data_ptr(), dt, w.data_ptr(),
-          _ptr(dy2), _ptr(w2), offsets.data_ptr(), out.data_ptr(), _DT[out.dtype], at, nws,
-          _status(status))
+    _need(two == (w2 is not None), "dy2 and w2 come together")
+    if two:
+        _need(dy2.shape == ys and w2.shape == wsh, "dy2 and w2 must match dy and w")
+    operands = (dy, w, dy2, w2) if two else (dy, w)
+    dt = _dtype(*operands)
+    (rows, n), k = ys, wsh[2]
+    out, odt = _out(out, out_dtype, dy.dtype, dev, rows, k)
+    shape, ws, at, nws = _plan("moe_grouped_linear_dx_workspace_size", dev, G, n, k, rows, dt, operands,
+                               int(two))
+    _call(dev, "moe_grouped_linear_dx", shape, dy.data_ptr(), dt, w.data_ptr(), _ptr(dy2), _ptr(w2),
+          offsets.data_ptr(), out.data_ptr(), odt, at, nws, _status(status))
     return out
 
 
@@ -197,17 +207,16 @@ def grouped_linear_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
     (dy's dtype unless out_dtype); zero for a group without rows."""
     dev = _check(dy, x, offsets, out, status)
     G = _groups(offsets)
-    _need(dy.dim() == 2 and x.dim() == 2 and x.shape[0] == dy.shape[0],
-          "dy must be [rows, n] and x [rows, k]")
+    ys, xs = dy.shape, x.shape
+    if len(ys) != 2 or len(xs) != 2 or xs[0] != ys[0]:
+        raise ValueError("dy must be [rows, n] and x [rows, k]")
     _need(out is not None or not accumulate, "accumulate needs out")
     dt = _dtype(dy, x)
-    (rows, n), k = dy.shape, x.shape[1]
-    out = _out(out, (G, n, k), out_dtype or (dy.dtype if out is None else out.dtype), dev)
-    shape = MoEGroupedShape(G, n, k, rows)
-    ws, at, nws = _workspace("moe_grouped_linear_dw_workspace_size", shape, dt, dev, (dy, x))
-    _call(dev, "moe_grouped_linear_dw", ctypes.byref(shape), dy.data_ptr(), dt, x.data_ptr(),
-          offsets.data_ptr(), out.data_ptr(), _DT[out.dtype], int(accumulate), at, nws,
-          _status(status))
+    (rows, n), k = ys, xs[1]
+    out, odt = _out(out, out_dtype, dy.dtype, dev, G, n, k)
+    shape, ws, at, nws = _plan("moe_grouped_linear_dw_workspace_size", dev, G, n, k, rows, dt, (dy, x))
+    _call(dev, "moe_grouped_linear_dw", shape, dy.data_ptr(), dt, x.data_ptr(), offsets.data_ptr(),
+          out.data_ptr(), odt, int(accumulate), at, nws, _status(status))
     return out
 
 
@@ -215,15 +224,17 @@ def _blocks(k: int) -> int:
     return -(-k // SCALE_BLOCK)
 
 
-def _empty_ckpt(rows: int, k: int, dev) -> Checkpoint:
-    return Checkpoint(torch.empty(rows, k, dtype=torch.uint8, device=dev),
-                      torch.empty(rows, _blocks(k), dtype=torch.uint8, device=dev))
+def _empty_ckpt(rows: int, k: int, dev: int) -> Checkpoint:
+    u8 = torch.uint8
+    return Checkpoint(torch.empty(rows, k, dtype=u8, device=dev),
+                      torch.empty(rows, _blocks(k), dtype=u8, device=dev))
 
 
 def _check_ckpt(c: Checkpoint, rows: int, k: int) -> None:
-    _need(c.codes.dtype == torch.uint8 and c.exps.dtype == torch.uint8
-          and tuple(c.codes.shape) == (rows, k) and tuple(c.exps.shape) == (rows, _blocks(k)),
-          "a checkpoint holds uint8 codes [rows, k] and exps [rows, ceil(k / 32)]")
+    codes, exps = c.codes, c.exps
+    if (codes.dtype != torch.uint8 or exps.dtype != torch.uint8 or codes.shape != (rows, k)
+            or exps.shape != (rows, _blocks(k))):
+        raise ValueError("a checkpoint holds uint8 codes [rows, k] and exps [rows, ceil(k / 32)]")
 
 
 def checkpoint_rows(src: torch.Tensor) -> Checkpoint:
@@ -250,9 +261,9 @@ def restore_rows(ckpt: Checkpoint, index: Optional[torch.Tensor] = None, *,
     if index is not None:
         _need(index.dtype == torch.int32 and index.dim() == 1, "index must be int32 [n]")
     n = rows if index is None else index.numel()
-    out = _out(out, (n, k), dtype if out is None else out.dtype, dev)
+    out, odt = _out(out, None, dtype, dev, n, k)
     _call(dev, "moe_restore_rows", ckpt.codes.data_ptr(), ckpt.exps.data_ptr(), rows, k,
-          _ptr(index), n, out.data_ptr(), _DT[out.dtype], _status(status))
+          _ptr(index), n, out.data_ptr(), odt, _status(status))
     return out
 
 
@@ -263,15 +274,16 @@ def swiglu_checkpoint(x: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, offse
     w1, w3 [groups, n, k]."""
     dev = _check(x, w1, w3, offsets, status)
     G = _groups(offsets)
-    _need(x.dim() == 2 and w1.dim() == 3 and w1.shape[0] == G and w1.shape[2] == x.shape[1]
-          and w3.shape == w1.shape, "x must be [rows, k], w1 and w3 [groups, n, k]")
-    dt = _dtype(x, w1, w3)
-    rows, n = x.shape[0], w1.shape[1]
+    xs, wsh = x.shape, w1.shape
+    if len(xs) != 2 or len(wsh) != 3 or wsh[0] != G or wsh[2] != xs[1] or w3.shape != wsh:
+        raise ValueError("x must be [rows, k], w1 and w3 [groups, n, k]")
+    operands = (x, w1, w3)
+    dt = _dtype(*operands)
+    (rows, k), n = xs, wsh[1]
     h = torch.empty(rows, n, dtype=x.dtype, device=dev)
     a, u = _empty_ckpt(rows, n, dev), _empty_ckpt(rows, n, dev)
-    shape = MoEGroupedShape(G, n, x.shape[1], rows)
-    ws, at, nws = _workspace("moe_swiglu_checkpoint_workspace_size", shape, dt, dev, (x, w1, w3))
-    _call(dev, "moe_swiglu_checkpoint", ctypes.byref(shape), x.data_ptr(), dt, w1.data_ptr(),
+    shape, ws, at, nws = _plan("moe_swiglu_checkpoint_workspace_size", dev, G, n, k, rows, dt, operands)
+    _call(dev, "moe_swiglu_checkpoint", shape, x.data_ptr(), dt, w1.data_ptr(),
           w3.data_ptr(), offsets.data_ptr(), h.data_ptr(), a.codes.data_ptr(), a.exps.data_ptr(),
           u.codes.data_ptr(), u.exps.data_ptr(), at, nws, _status(status))
     return h, a, u
@@ -285,19 +297,20 @@ def swiglu_backward(dy: torch.Tensor, w2: torch.Tensor, a: Checkpoint, u: Checkp
     -> da, du, hg [rows, n] in dy's dtype, dgate [rows] fp32."""
     dev = _check(dy, w2, a.codes, a.exps, u.codes, u.exps, gate, offsets, status)
     G = _groups(offsets)
-    _need(dy.dim() == 2 and w2.dim() == 3 and w2.shape[0] == G and w2.shape[1] == dy.shape[1],
-          "dy must be [rows, k] and w2 [groups, k, n]")
+    ys, wsh = dy.shape, w2.shape
+    if len(ys) != 2 or len(wsh) != 3 or wsh[0] != G or wsh[1] != ys[1]:
+        raise ValueError("dy must be [rows, k] and w2 [groups, k, n]")
     dt = _dtype(dy, w2)
-    (rows, k), n = dy.shape, w2.shape[2]
+    (rows, k), n = ys, wsh[2]
     _check_ckpt(a, rows, n)
     _check_ckpt(u, rows, n)
     if gate is not None:
         _need(gate.dtype == torch.float32 and tuple(gate.shape) == (rows,), "gate must be fp32 [rows]")
-    da, du, hg = (torch.empty(rows, n, dtype=dy.dtype, device=dev) for _ in range(3))
+    dtype = dy.dtype
+    da, du, hg = (torch.empty(rows, n, dtype=dtype, device=dev) for _ in range(3))
     dgate = torch.empty(rows, dtype=torch.float32, device=dev)
-    shape = MoEGroupedShape(G, n, k, rows)
-    ws, at, nws = _workspace("moe_swiglu_backward_workspace_size", shape, dt, dev, (dy, w2))
-    _call(dev, "moe_swiglu_backward", ctypes.byref(shape), dy.data_ptr(), dt, w2.data_ptr(),
+    shape, ws, at, nws = _plan("moe_swiglu_backward_workspace_size", dev, G, n, k, rows, dt, (dy, w2))
+    _call(dev, "moe_swiglu_backward", shape, dy.data_ptr(), dt, w2.data_ptr(),
           a.codes.data_ptr(), a.exps.data_ptr(), u.codes.data_ptr(), u.exps.data_ptr(), _ptr(gate),
           offsets.data_ptr(), da.data_ptr(), du.data_ptr(), hg.data_ptr(), dgate.data_ptr(),
           at, nws, _status(status))
@@ -313,9 +326,9 @@ def gather_rows(src: torch.Tensor, index: torch.Tensor, *, dtype: Optional[torch
           "src must be [rows, k] and index int32 [n]")
     dt = _dtype(src)
     (rows, k), n = src.shape, index.numel()
-    out = _out(None, (n, k), dtype or src.dtype, dev)
+    out, odt = _out(None, dtype, src.dtype, dev, n, k)
     _call(dev, "moe_gather_rows", src.data_ptr(), dt, rows, k, index.data_ptr(), n, out.data_ptr(),
-          _DT[out.dtype], _status(status))
+          odt, _status(status))
     return out
 
 
