@@ -693,7 +693,7 @@ MOE_EXPORT moe_status moe_checkpoint_rows(const void *src, moe_dtype dt, int64_t
       ckpt::save_rows_v8<<<grid, ckpt::ROW_THREADS, 0, cs>>>(static_cast<const bf16 *>(src), rows, k, codes, exps);
     return launch_status();
   }
-  const unsigned grid = row_grid(rows * nb);
+  const unsigned grid = row_grid(rows * ((nb + ckpt::UNROLL - 1) / ckpt::UNROLL));
   if (dt == MOE_F32)
     ckpt::save_rows<<<grid, ckpt::ROW_THREADS, 0, cs>>>(static_cast<const float *>(src), rows, k, codes, exps);
   else
@@ -722,7 +722,7 @@ MOE_EXPORT moe_status moe_restore_rows(const uint8_t *codes, const uint8_t *exps
       ckpt::load_rows_v8<<<grid, ckpt::ROW_THREADS, 0, cs>>>(codes, exps, rows, k, index, n, static_cast<bf16 *>(out), dev_status);
     return launch_status();
   }
-  const unsigned grid = row_grid(n * nb);
+  const unsigned grid = row_grid(n * ((nb + ckpt::UNROLL - 1) / ckpt::UNROLL));
   if (out_dt == MOE_F32)
     ckpt::load_rows<<<grid, ckpt::ROW_THREADS, 0, cs>>>(codes, exps, rows, k, index, n, static_cast<float *>(out), dev_status);
   else
