@@ -314,6 +314,26 @@ def test_checkpoint_rows(k, dtype):
             assert torch.equal(r[f], w[f].to(out))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("k", [255, 256])
+def test_every_code_with_every_scale(k, dtype):
+    # row e holds the codes under the scale byte e; NaN codes make their blocks
+    # take another way, so the rows come without them too
+    codes = torch.arange(256, dtype=torch.int16).repeat(256, 1)[:, :k]
+    finite = torch.where((codes & 0x7F) == 0x7F, codes - 1, codes)
+    codes = torch.cat([codes, finite]).to(torch.uint8).contiguous()
+    exps = torch.arange(256).to(torch.uint8).repeat(2)[:, None].repeat(1, (k + 31) // 32).contiguous()
+    got = moe.restore_rows(moe.Checkpoint(codes.cuda(), exps.cuda()), dtype=dtype).cpu()
+    # 2^(byte - 127) in 64 bits; byte 255 reads as an infinity, which makes zeros NaN
+    scale = torch.ldexp(torch.ones(512, 1, dtype=torch.float64), exps[:, :1].int() - 127)
+    scale[exps[:, :1] == 255] = float("inf")
+    want = (codes.view(torch.float8_e4m3fn).double() * scale).to(torch.float32).to(dtype)
+    assert torch.equal(got.isnan(), want.isnan())
+    ok = ~want.isnan()
+    assert torch.equal(got[ok], want[ok])
+    assert torch.equal(got[ok].signbit(), want[ok].signbit())
+
+
 def test_restore_rows_refuses_bad_indices():
     v = R.normal(1, 10, 96)
     c = moe.checkpoint_rows(v.cuda())
