@@ -80,7 +80,8 @@ __device__ __forceinline__ float sigmoid<bf16>(float a) {
 
 template <typename T>
 struct Vec8;  // eight values, loaded or stored as 16-byte vectors; bf16 rows with
-              // streaming stores (32768 x 7168 restored in 92 us, 106 without)
+              // streaming stores (32768 x 7168 restored in 92 us, 106 without, both
+              // with one resident set of blocks)
 template <>
 struct Vec8<bf16> {
   static __device__ __forceinline__ void load(const bf16 *p, float (&v)[8]) {
@@ -124,7 +125,8 @@ __device__ __forceinline__ int64_t item_row(int64_t un, int per) {
 }
 
 constexpr int ROW_THREADS = 256;
-constexpr int UNROLL = 4;  // loads in flight per lane: eight values each, or one
+constexpr int UNROLL = 4;   // loads in flight per lane, of eight values each
+constexpr int UNROLL1 = 8;  // and of one value
 
 // Eight values a lane, four lanes a block: k % 8 == 0 and aligned rows.
 template <typename TI>
@@ -173,28 +175,28 @@ __global__ void __launch_bounds__(ROW_THREADS) save_rows_v8(const TI *__restrict
   }
 }
 
-// One value a lane, a block a warp, UNROLL blocks in flight: any k and
-// alignment. Bound by the latency of its loads: with one block in flight,
-// 4000 rows of 2313 took 29.3 us to save and 13649 of them 114 us to restore;
-// with four 18.4 and 57.5 us.
+// One value a lane, a block a warp, UNROLL1 blocks in flight: any k and
+// alignment. Bound by the latency of its loads: 13649 rows of 2313 are restored
+// in 114 us with one block in flight, 55 with four, 47.5 with eight and 51 with
+// sixteen; 4000 of them are saved in 29, 18, 19 and 21 us.
 template <typename TI>
 __global__ void __launch_bounds__(ROW_THREADS) save_rows(const TI *__restrict__ src, int64_t rows,
                                                          int k, uint8_t *__restrict__ codes,
                                                          uint8_t *__restrict__ exps) {
-  const int lane = threadIdx.x % 32, nb = (k + BLOCK - 1) / BLOCK, per = (nb + UNROLL - 1) / UNROLL;
+  const int lane = threadIdx.x % 32, nb = (k + BLOCK - 1) / BLOCK, per = (nb + UNROLL1 - 1) / UNROLL1;
   const int64_t units = rows * per, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
        un += step) {
     const int64_t row = item_row(un, per);
-    const int b0 = (int)(un - row * per) * UNROLL;
-    float v[UNROLL];
+    const int b0 = (int)(un - row * per) * UNROLL1;
+    float v[UNROLL1];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < UNROLL1; ++u) {
       const int i = (b0 + u) * BLOCK + lane;
       v[u] = i < k ? to_f(src[row * k + i]) : 0.0f;
     }
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < UNROLL1; ++u) {
       const int i = (b0 + u) * BLOCK + lane;
       const int e = scale_byte(__reduce_max_sync(0xffffffffu, finite_bits(v[u])));
       if (i < k) codes[row * k + i] = encode1(v[u], inv_scale_of(e));
@@ -265,22 +267,22 @@ __global__ void __launch_bounds__(ROW_THREADS) load_rows(const uint8_t *__restri
                                                          const int32_t *__restrict__ index,
                                                          int64_t n, TO *__restrict__ out,
                                                          int32_t *status) {
-  const int lane = threadIdx.x % 32, nb = (k + BLOCK - 1) / BLOCK, per = (nb + UNROLL - 1) / UNROLL;
+  const int lane = threadIdx.x % 32, nb = (k + BLOCK - 1) / BLOCK, per = (nb + UNROLL1 - 1) / UNROLL1;
   const int64_t units = n * per, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
        un += step) {
     const int64_t i = item_row(un, per), row = source_row(index, i, rows, status);
-    const int b0 = (int)(un - i * per) * UNROLL;
-    uint8_t c[UNROLL], e[UNROLL];
+    const int b0 = (int)(un - i * per) * UNROLL1;
+    uint8_t c[UNROLL1], e[UNROLL1];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < UNROLL1; ++u) {
       const int j = (b0 + u) * BLOCK + lane;
       const bool on = row >= 0 && j < k;
       c[u] = on ? codes[row * k + j] : 0;
       e[u] = on ? exps[row * nb + b0 + u] : 0;
     }
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < UNROLL1; ++u) {
       const int j = (b0 + u) * BLOCK + lane;
       if (j < k) out[i * k + j] = from_f<TO>(decode1(c[u], scale_of(e[u])));
     }
@@ -289,37 +291,38 @@ __global__ void __launch_bounds__(ROW_THREADS) load_rows(const uint8_t *__restri
 
 // ------------------------------------------------------------ plain rows
 
-// out[i] = src[index[i]], eight values a lane (VEC) or one.
+// out[i] = src[index[i]], eight values a lane (VEC) or one (32768 rows of 2313
+// bf16 values: 49 us with eight loads in flight, 66 with four).
 template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(ROW_THREADS) gather_rows(const TI *__restrict__ src, int64_t rows,
                                                            int k, const int32_t *__restrict__ index,
                                                            int64_t n, TO *__restrict__ out,
                                                            int32_t *status) {
-  constexpr int V = VEC ? 8 : 1, PER = 32 * UNROLL * V;  // values of an item
+  constexpr int V = VEC ? 8 : 1, U = VEC ? UNROLL : UNROLL1, PER = 32 * U * V;  // values of an item
   const int lane = threadIdx.x % 32, items = (k + PER - 1) / PER;
   const int64_t units = n * items, step = (int64_t)gridDim.x * (ROW_THREADS / 32);
   for (int64_t un = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32; un < units;
        un += step) {
     const int64_t i = item_row(un, items), row = source_row(index, i, rows, status);
     const int c0 = (int)(un - i * items) * PER + lane * V;
-    float v[UNROLL][8];
+    float v[U][V];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int c = c0 + u * 32 * V;
 #pragma unroll
       for (int j = 0; j < V; ++j) v[u][j] = 0.0f;
       if (row >= 0 && c < k) {
-        if (VEC)
+        if constexpr (VEC)
           Vec8<TI>::load(src + row * k + c, v[u]);
         else
           v[u][0] = to_f(src[row * k + c]);
       }
     }
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int c = c0 + u * 32 * V;
       if (c >= k) continue;
-      if (VEC)
+      if constexpr (VEC)
         Vec8<TO>::store(out + i * k + c, v[u]);
       else
         out[i * k + c] = from_f<TO>(v[u][0]);
