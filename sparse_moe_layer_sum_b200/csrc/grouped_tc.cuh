@@ -259,12 +259,17 @@ constexpr int SEG = 512 / BK;
 // arithmetic that takes the MMAs of several segments, and the MMAs may run two
 // segments ahead of it: in a long contraction its first two are twice as long
 // (636 -> 596 us over 32 groups, 16384 rows; error 6e-7 instead of 5e-7).
-// UP's codes change with the sums' last bits near a border; over a short
+// UP's codes change with the sums' last bits near a border. Over a short
 // contraction, where plain fp32 sums are better than that, its segments are
-// half as long.
+// shorter: of 1e9 codes of a 256-deep contraction 3200 differ from exact sums'
+// codes with 64 values a segment, 4400 with 128, 7000 with 256 and 4000 with
+// plain fp32 sums; 512 deep 5000 with 128, 8300 with 256 and 5900 with plain
+// sums. It costs time only where the read-out shows, in many rows (16 groups,
+// 16000 rows, to 1024: from 512 102 us with 128, 89 with 256; from 256 92 with
+// 64, 79 with 256; 8 groups, 2000 rows, 256 -> 256 12.9 and 12.5).
 template <int OP>
 __device__ __forceinline__ int segment(int i, int nkb) {
-  if (OP == UP && nkb <= 32) return SEG / 2;
+  if (OP == UP && nkb <= 32) return nkb <= 4 ? SEG / 8 : nkb <= 8 ? SEG / 4 : SEG / 2;
   return OP == BWD && i < 2 && nkb >= 64 ? 2 * SEG : SEG;
 }
 
