@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full + s, 2);
-      mbar_init(empty + s, 1);
+      mbar_init(empty + s, 2);  // the MMAs, and the warp of the tail rows
       mbar_init(tail + s, 1);
       pending[s] = -1;
     }
@@ -1079,6 +1079,9 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
       // ------------------------------------------- tail rows, ahead of the MMAs
       // (done by the issuing warp itself, this held up every tile of a short
       // group: 455 -> 385 us for 32 groups of about 128 rows)
+      // The warp passes every block and counts on `empty` as the MMAs do: were
+      // it a ring behind the producer, `tail` would have gone through two
+      // phases, which their one parity bit does not tell from none.
       Ring r;
       for (int64_t tile = unit; tile < total; tile += nunits) {
         const Job j = job(tile);
@@ -1102,6 +1105,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
               arrive_cluster(mapa_shared(smem_u32(full + r.stage), 0));
             }
           }
+          if (lane == 0) mbar_arrive(empty + r.stage);
           r.next(STAGES);
         }
       }
