@@ -196,9 +196,18 @@ def experts_forward_combine(shape: BlockShape, x: torch.Tensor, wstruct: MoEExpe
 def combine(shape: BlockShape, weights: torch.Tensor, slot_of: torch.Tensor,
             out_perm: torch.Tensor, out_shared: Optional[torch.Tensor], *, y=None, status=None):
     """moe_combine: y [T, dim] fp32."""
-    _check_cuda(weights, slot_of, out_perm, out_shared)
-    cfg = shape.cfg()
     T = weights.shape[0]
+    routed = T * shape.topk
+    # what the kernel reads, which has only T to go by
+    if (weights.numel() < routed or slot_of.numel() < routed or out_perm.numel() < routed * shape.dim
+            or (shape.n_shared and (out_shared is None or out_shared.numel() < T * shape.dim))
+            or (y is not None and y.numel() < T * shape.dim)):
+        raise ValueError("weights, slot_of, out_perm, out_shared and y must be of one batch")
+    if slot_of.dtype != torch.int32 or any(t is not None and t.dtype != torch.float32
+                                           for t in (weights, out_perm, out_shared, y)):
+        raise ValueError("slot_of must be int32, the others fp32")
+    _check_cuda(weights, slot_of, out_perm, out_shared, y)
+    cfg = shape.cfg()
     if y is None:
         y = torch.empty(T, shape.dim, dtype=torch.float32, device=weights.device)
     st = fn("moe_combine", "moe_combine")(

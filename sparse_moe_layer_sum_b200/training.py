@@ -406,6 +406,8 @@ def experts_training_forward(shape: BlockShape, params: BlockParams, x: torch.Te
     _need(x.dim() == 2 and x.shape[1] == shape.dim, "x must be [T, dim]")
     _need(params.w1.dtype == x.dtype and x.dtype in _DT, "training takes weights in x's dtype")
     T, k = x.shape[0], shape.topk
+    _need(tuple(weights.shape) == (T, k) and sorted_token.numel() == slot_of.numel() == T * k,
+          "the routing is not that of x's T rows")
     row_token, row_gate, group_offsets = training_rows(shape, weights, offsets, sorted_token, slot_of,
                                                        status=status)
     rows = gather_rows(x, row_token, status=status)
@@ -425,6 +427,11 @@ def experts_training_backward(shape: BlockShape, params: BlockParams, saved: Sav
     dw1, dw3 and dw2; otherwise they are new tensors of grad_dtype."""
     T, k = saved.x.codes.shape[0], shape.topk
     _need(tuple(dy.shape) == (T, shape.dim), "dy must be [T, dim]")
+    # (combine and the gathers below go by T, topk and the saved lists together)
+    _need(saved.slot_of.numel() == T * k
+          and saved.row_token.numel() == saved.row_gate.numel() == T * (k + shape.n_shared)
+          and saved.group_offsets.numel() == shape.n_routed + shape.n_shared + 1,
+          "saved is not of a batch of this shape")
     st = dict(status=status)
     off = saved.group_offsets
     dyr = gather_rows(dy, saved.row_token, dtype=saved.dtype, **st)

@@ -1,0 +1,82 @@
+"""Calls of the training binding that are refused before anything reaches the
+GPU, so that they are tested without one."""
+import pytest
+import torch
+
+import sparse_moe_layer_sum_b200 as moe
+
+SHAPE = moe.BlockShape(dim=64, n_routed=8, n_groups=2, topk_groups=1, topk=2, inter=32, n_shared=0)
+SHARED = moe.BlockShape(dim=64, n_routed=8, n_groups=2, topk_groups=1, topk=2, inter=32, n_shared=1)
+
+
+def params(shape):
+    G = shape.n_routed + shape.n_shared
+    w = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    return moe.BlockParams(torch.zeros(shape.n_routed, shape.dim), None, w(G, shape.inter, shape.dim),
+                           w(G, shape.inter, shape.dim), w(G, shape.dim, shape.inter))
+
+
+def routing(shape, T):
+    i32 = torch.int32
+    return (torch.zeros(T, shape.topk), torch.zeros(shape.n_routed + 1, dtype=i32),
+            torch.zeros(T * shape.topk, dtype=i32), torch.zeros(T * shape.topk, dtype=i32))
+
+
+def saved(shape, T, slots=None, rows=None):
+    u8, i32 = torch.uint8, torch.int32
+    R = T * (shape.topk + shape.n_shared) if rows is None else rows
+    ckpt = lambda n, k: moe.Checkpoint(torch.zeros(n, k, dtype=u8), torch.zeros(n, -(-k // 32), dtype=u8))
+    return moe.SavedExperts(ckpt(T, shape.dim), ckpt(R, shape.inter), ckpt(R, shape.inter),
+                            torch.zeros(R, dtype=i32), torch.zeros(R),
+                            torch.zeros(shape.n_routed + shape.n_shared + 1, dtype=i32),
+                            torch.zeros(T * shape.topk if slots is None else slots, dtype=i32),
+                            torch.bfloat16)
+
+
+@pytest.mark.parametrize("shape", [SHAPE, SHARED], ids=["routed", "shared"])
+@pytest.mark.parametrize("T", [7, 9, 16])
+def test_forward_takes_the_routing_of_its_own_rows(shape, T):
+    """x of more or fewer tokens than the routing was made for."""
+    x = torch.zeros(T, shape.dim, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="routing"):
+        moe.experts_training_forward(shape, params(shape), x, *routing(shape, 8))
+    # the weights of T tokens with the lists of 8
+    with pytest.raises(ValueError, match="routing"):
+        moe.experts_training_forward(shape, params(shape), x, torch.zeros(T, shape.topk),
+                                     *routing(shape, 8)[1:])
+
+
+@pytest.mark.parametrize("shape", [SHAPE, SHARED], ids=["routed", "shared"])
+def test_backward_takes_lists_of_the_saved_batch(shape):
+    dy = torch.zeros(16, shape.dim)
+    p = params(shape)
+    R = 8 * (shape.topk + shape.n_shared)
+    for s in (saved(shape, 16, slots=8 * shape.topk), saved(shape, 16, rows=R),
+              saved(shape, 16, slots=8 * shape.topk, rows=R),
+              saved(SHAPE if shape is SHARED else SHARED, 16)):
+        with pytest.raises(ValueError, match="saved"):
+            moe.experts_training_backward(shape, p, s, dy)
+
+
+@pytest.mark.parametrize("shape", [SHAPE, SHARED], ids=["routed", "shared"])
+def test_combine_reads_within_its_operands(shape):
+    T, n = 8, 8 * shape.topk
+    good = dict(weights=torch.zeros(T, shape.topk), slot_of=torch.zeros(n, dtype=torch.int32),
+                out_perm=torch.zeros(n, shape.dim),
+                out_shared=torch.zeros(T, shape.dim) if shape.n_shared else None)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.combine(shape, **good)
+    bad = dict(weights=torch.zeros(T, 1), slot_of=good["slot_of"][:-1], out_perm=good["out_perm"][:-1],
+               y=torch.zeros(T - 1, shape.dim))
+    if shape.n_shared:
+        bad["out_shared"] = good["out_shared"][:-1]
+    for name, v in bad.items():
+        with pytest.raises(ValueError, match="one batch"):
+            moe.combine(shape, **{**good, name: v})
+    if shape.n_shared:
+        with pytest.raises(ValueError, match="one batch"):
+            moe.combine(shape, **{**good, "out_shared": None})
+    for name, v in (("out_perm", good["out_perm"].bfloat16()), ("slot_of", good["slot_of"].short()),
+                    ("y", torch.zeros(T, shape.dim, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError, match="fp32"):
+            moe.combine(shape, **{**good, name: v})
