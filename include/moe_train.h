@@ -16,8 +16,9 @@
  *    Groups may be empty.  Rows outside offsets[0] .. offsets[groups] are
  *    neither read into a result nor written.
  *  - Offsets that decrease or leave [0, rows] are clamped on the device, so
- *    that no access leaves a buffer; MOE_ERR_RANGE goes to dev_status and
- *    the outputs of that call are unspecified.
+ *    that no access leaves a buffer and no row is in two groups;
+ *    MOE_ERR_RANGE goes to dev_status and the outputs of that call are
+ *    unspecified.
  *  - Operands are MOE_BF16 or MOE_F32, both operands of a product the same.
  *    Sums are fp32 and rounded once at the end.
  *  - No atomics: results do not depend on the order in which blocks run.

@@ -27,7 +27,7 @@ __device__ __forceinline__ void group_bounds(const int32_t *__restrict__ off, in
   n = (int)(cb - ca);
 }
 
-// Group g's rows are lo[g] .. lo[g + 1] - 1 (none where that runs backwards).
+// Group g's rows are lo[g] .. lo[g + 1] - 1.
 // They are cut into ntt tiles of `base` rows, a multiple of 16 and at most
 // rows_max; each token tile meets ft feature tiles.  start is the exclusive
 // prefix of ntt * ft over the groups; start[G] the number of tiles.
@@ -38,7 +38,7 @@ struct Table {
   static size_t bytes(int G) { return sizeof(int32_t) * (size_t)(2 * G + 2); }
   __device__ __forceinline__ Table(void *mem, int G, int rows_max_)
       : start(static_cast<int32_t *>(mem)), lo(start + G + 1), rows_max(rows_max_) {}
-  __device__ __forceinline__ int rows(int g) const { return max(0, lo[g + 1] - lo[g]); }
+  __device__ __forceinline__ int rows(int g) const { return lo[g + 1] - lo[g]; }
 };
 
 __device__ __forceinline__ void split_rows(int n, int rows_max, int &base, int &ntt) {
@@ -55,12 +55,21 @@ __device__ __forceinline__ void split_rows(int n, int rows_max, int &base, int &
 // Every thread of the block calls; ends with the table complete for all.
 __device__ __forceinline__ void build_table(const Table &t, const int32_t *__restrict__ off, int G,
                                             int64_t rows, int ft, int32_t *status) {
+  bool bad = false;
   for (int g = threadIdx.x; g <= G; g += blockDim.x) {
     const int64_t a = off[g];
-    if (a < 0 || a > rows || (g < G && off[g + 1] < a)) set_status(status, MOE_ERR_RANGE);
+    bad |= a < 0 || a > rows || (g < G && off[g + 1] < a);
     t.lo[g] = (int)(a < 0 ? 0 : a > rows ? rows : a);
   }
-  __syncthreads();
+  if (bad) set_status(status, MOE_ERR_RANGE);
+  // An offset below an earlier one counts as the earlier one: no row is then in
+  // two groups, and the groups have no more tiles than rows give, which the
+  // 32-bit tile numbers hold.
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0)
+      for (int g = 1; g <= G; ++g) t.lo[g] = max(t.lo[g], t.lo[g - 1]);
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {  // exclusive prefix: a lane owns a run of groups
     const int lane = threadIdx.x, per = (G + 31) / 32;
     const int g0 = min(G, lane * per), g1 = min(G, g0 + per);

@@ -39,3 +39,27 @@ def test_dw_of_long_groups_that_end_inside_a_step(dtype, out):
     R.assert_close(got, *R.dw(dy, x, off))
     again = moe.grouped_linear_dw(dy.cuda(), x.cuda(), offs(off), out_dtype=out)
     assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad,good", [([0, 40, 10, 60], [0, 40, 40, 60]),
+                                      ([0, 60, 0, 60, 0, 60], [0] + [60] * 5),
+                                      ([70, 5, -3, 10 ** 9, 40], [60] * 5)])
+def test_a_row_has_one_group_whatever_the_offsets(bad, good, dtype):
+    """Offsets that turn back: an offset below an earlier one counts as the
+    earlier one, so that no row is written twice and the tiles are bounded by
+    the rows (1024 groups that turn back over 2^20 rows, 32768 features: 2^31
+    tiles of 64 x 128, more than their 32-bit numbers hold)."""
+    G, n, k = len(bad) - 1, 96, 128
+    x, w = R.normal(1, 60, k, dtype=dtype), R.normal(2, G, n, k, dtype=dtype, std=k ** -0.5)
+    dy = R.normal(3, 60, n, dtype=dtype)
+    a = moe.checkpoint_rows(R.normal(4, 60, k, dtype=dtype).cuda())
+    for call in (lambda o, s: [moe.grouped_linear(x.cuda(), w.cuda(), o, status=s)],
+                 lambda o, s: [moe.grouped_linear_dx(dy.cuda(), w.cuda(), o, status=s)],
+                 lambda o, s: [moe.swiglu_checkpoint(x.cuda(), w.cuda(), w.cuda(), o, status=s)[0]],
+                 lambda o, s: moe.swiglu_backward(dy.cuda(), w.cuda(), a, a, o, status=s)):
+        s1, s2 = status(), status()
+        got, want = call(offs(bad), s1), call(offs(good), s2)
+        assert int(s1.item()) == -6 and int(s2.item()) == 0
+        for t, v in zip(got, want):
+            assert torch.equal(t[good[0]:good[-1]], v[good[0]:good[-1]])
