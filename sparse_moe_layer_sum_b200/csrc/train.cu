@@ -885,7 +885,8 @@ MOE_EXPORT moe_status moe_training_rows(const moe_cfg *cfg, int64_t T, const int
   const moe_status st = check_cfg(cfg);
   if (st != MOE_OK) return st;
   if (T < 0) return MOE_ERR_INVALID;
-  if (cfg->n_shared > 1 || T * ((int64_t)cfg->topk + cfg->n_shared) >= ((int64_t)1 << 31))
+  if (cfg->n_shared > 1 || T >= ((int64_t)1 << 31) ||  // (the product below would wrap)
+      T * ((int64_t)cfg->topk + cfg->n_shared) >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
   if (!offsets || !group_offsets) return MOE_ERR_INVALID;
   if (T > 0 && (!sorted_token || !slot_of || !weights || !row_token || !row_gate))

@@ -80,3 +80,17 @@ def test_combine_reads_within_its_operands(shape):
                     ("y", torch.zeros(T, shape.dim, dtype=torch.bfloat16))):
         with pytest.raises(ValueError, match="fp32"):
             moe.combine(shape, **{**good, name: v})
+
+
+def test_training_rows_of_a_wrapping_token_count():
+    """T * (topk + n_shared) past 64 bits: 2^61 * 8 is 0 there."""
+    import ctypes
+    from sparse_moe_layer_sum_b200 import build
+    from sparse_moe_layer_sum_b200._lib import MoECfg, fn
+    build.build_all()
+    p = ctypes.c_void_p(0x1000)                     # never dereferenced
+    cfg = MoECfg(dim=64, n_routed=8, n_groups=1, topk_groups=1, topk=7, inter=32, n_shared=1,
+                 route_scale=2.5, score_func=0, has_bias=1)
+    for T in (1 << 61, 1 << 62, (1 << 61) + 1):
+        assert fn("moe_train", "moe_training_rows")(ctypes.byref(cfg), T, p, p, p, p, p, p, p, None,
+                                                    None) == -2
