@@ -26,7 +26,8 @@
  *    are 16-byte aligned run on the tcgen05 tensor cores as they are.  Other
  *    products of some size do through copies in the workspace: bf16 rows
  *    padded, fp32 operands split into three bf16 terms (results as exact as
- *    fp32 sums; a result that depends on an infinite fp32 operand may be NaN).
+ *    fp32 sums of operands that are multiples of 2^-133, as all above 2^-110
+ *    are; a result that depends on an infinite fp32 operand may be NaN).
  *    Small ones, and any without a workspace, run on the CUDA cores with fp32
  *    multiply-adds.
  *  - Each *_workspace_size takes `aligned`: 1 when every operand of the call

@@ -198,8 +198,11 @@ __device__ __forceinline__ int term_a(int q) { return (0x118 >> (2 * q)) & 3; } 
 __device__ __forceinline__ int term_b(int q) { return (0x052 >> (2 * q)) & 3; }  // 2 0 1 1 0 0
 
 // src [rows, k] into TERMS planes [rows, kp] of bf16, kp = k rounded up to 8,
-// zeros behind k.  One term is a copy (rounded, for fp32 src).  A value that is
-// not finite, or rounds to infinity, stays in the first term alone.
+// zeros behind k.  One term is a copy (bf16 src).  A value that is not finite
+// stays in the first term alone.  A finite one above bf16's largest, which
+// would round to infinity, takes that largest as its first term and leaves the
+// rest to the others.  Bits below 2^-133, bf16's smallest step, are lost.
+constexpr float BF16_MAX = 0x1.fep127f;
 template <typename TI, int TERMS>
 __global__ void __launch_bounds__(256) stage_rows(const TI *__restrict__ src, int64_t rows, int k,
                                                   int kp, bf16 *__restrict__ dst) {
@@ -213,9 +216,13 @@ __global__ void __launch_bounds__(256) stage_rows(const TI *__restrict__ src, in
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
       uint32_t w[4];
+      float q[8];  // what is rounded
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        q[j] = TERMS > 1 && isfinite(v[j]) ? fminf(fmaxf(v[j], -BF16_MAX), BF16_MAX) : v[j];
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j], v[j + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(q[j], q[j + 1]);
         w[j / 2] = *reinterpret_cast<const uint32_t *>(&h);
         if (t + 1 < TERMS) {
           const float2 f = __bfloat1622float2(h);

@@ -63,3 +63,45 @@ def test_a_row_has_one_group_whatever_the_offsets(bad, good, dtype):
         assert int(s1.item()) == -6 and int(s2.item()) == 0
         for t, v in zip(got, want):
             assert torch.equal(t[good[0]:good[-1]], v[good[0]:good[-1]])
+
+
+# wide, narrow and split tiles of the staged fp32 products
+STAGED = [([300, 900], 640, 1032), ([70, 0, 90], 640, 1100), ([700], 96, 2500)]
+
+
+@pytest.mark.parametrize("sizes,n,k", STAGED)
+def test_largest_finite_fp32_operands(sizes, n, k):
+    """Magnitudes between bf16's largest value and fp32's, which a first bf16
+    term would round to infinity, in the rows and in the weights."""
+    off, top = R.offsets_of(sizes), torch.finfo(F32).max
+    rows, G = off[-1], len(sizes)
+    assert float(torch.tensor(top).to(BF)) == float("inf")
+    x, dy = R.normal(1, rows, k, dtype=F32), R.normal(2, rows, n, dtype=F32)
+    w = R.normal(3, G, n, k, dtype=F32, std=2.0 ** -20)
+    x[60, 5], x[7, 0], x[60, 9] = 3.4e38, -top, 3.3962e38   # two of them in one sum: below 2^108 each
+    w[0, 11, 3], dy[7, 2] = top, -3.4e38
+    x[:, 3] *= 2.0 ** -20
+    dy[:, 11] *= 2.0 ** -20
+    st = status()
+    y = moe.grouped_linear(x.cuda(), w.cuda(), offs(off), status=st)
+    R.assert_close(y, *R.linear(x, w, off), "linear")
+    d = moe.grouped_linear_dx(dy.cuda(), w.cuda(), offs(off), status=st)
+    R.assert_close(d, *R.dx(dy, w, off), "dx")
+    xs = R.normal(4, rows, k, dtype=F32, std=2.0 ** -20)
+    R.assert_close(moe.grouped_linear_dw(dy.cuda(), xs.cuda(), offs(off), status=st), *R.dw(dy, xs, off), "dw")
+    w *= 2.0 ** -90                          # projections of at most 2^20 or so
+    h, *_ = moe.swiglu_checkpoint(x.cuda(), w.cuda(), w.cuda(), offs(off), status=st)
+    assert torch.isfinite(h).all()
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("sizes,n,k", STAGED)
+def test_smallest_fp32_operands(sizes, n, k):
+    """Operand bits below 2^-133 are lost, half a step of them at most a value."""
+    off = R.offsets_of(sizes)
+    x, w = R.normal(1, off[-1], k, dtype=F32), R.normal(2, len(sizes), n, k, dtype=F32)
+    x *= torch.exp2(torch.linspace(-135, -100, off[-1]))[:, None]
+    y = moe.grouped_linear(x.cuda(), w.cuda(), offs(off))
+    v, e = R.linear(x, w, off)
+    lost = R.linear(torch.ones_like(x), w.abs(), off)[0] * 2.0 ** -134
+    R.assert_close(y, v, e + 1.01 * lost)
