@@ -496,6 +496,14 @@ Plan plan_product(Kind kind, const moe_grouped_shape *s, const Operand *o, int n
   return p;
 }
 
+// Bytes of workspace that a product takes: with aligned operands, or with any
+// (aligned ones can take the more: parts of a tensor-core product).
+size_t product_workspace(Kind kind, const moe_grouped_shape *s, const Operand *o, int n, moe_dtype dt,
+                         int products, bool aligned) {
+  const size_t least = plan_product(kind, s, o, n, dt, products, true).total();
+  return aligned ? least : std::max(least, plan_product(kind, s, o, n, dt, products, false).total());
+}
+
 // The plan for operands whose addresses are known.  Without the workspace a
 // staged product runs on the CUDA cores, a direct one undivided.
 Plan plan_call(Kind kind, const moe_grouped_shape *s, const Operand *o, int n, moe_dtype dt, int products,
@@ -620,7 +628,7 @@ MOE_EXPORT size_t moe_grouped_linear_workspace_size(const moe_grouped_shape *s, 
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
   const int n = linear_ops(s, nullptr, nullptr, o);
-  return plan_product(K_LINEAR, s, o, n, dt, 1, aligned).total();
+  return product_workspace(K_LINEAR, s, o, n, dt, 1, aligned != 0);
 }
 
 MOE_EXPORT size_t moe_grouped_linear_dx_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
@@ -628,7 +636,7 @@ MOE_EXPORT size_t moe_grouped_linear_dx_workspace_size(const moe_grouped_shape *
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
   const int n = dx_ops(s, nullptr, nullptr, nullptr, nullptr, two != 0, o);
-  return plan_product(K_DX, s, o, n, dt, two ? 2 : 1, aligned).total();
+  return product_workspace(K_DX, s, o, n, dt, two ? 2 : 1, aligned != 0);
 }
 
 MOE_EXPORT size_t moe_grouped_linear_dw_workspace_size(const moe_grouped_shape *s, moe_dtype dt,
@@ -636,7 +644,7 @@ MOE_EXPORT size_t moe_grouped_linear_dw_workspace_size(const moe_grouped_shape *
   if (check_shape(s) != MOE_OK || !act_type(dt)) return 0;
   Operand o[4];
   const int n = dw_ops(s, nullptr, nullptr, o);
-  return plan_product(K_DW, s, o, n, dt, 1, aligned).total();
+  return product_workspace(K_DW, s, o, n, dt, 1, aligned != 0);
 }
 
 MOE_EXPORT moe_status moe_grouped_linear(const moe_grouped_shape *s, const void *x, moe_dtype dt,

@@ -94,3 +94,26 @@ def test_training_rows_of_a_wrapping_token_count():
     for T in (1 << 61, 1 << 62, (1 << 61) + 1):
         assert fn("moe_train", "moe_training_rows")(ctypes.byref(cfg), T, p, p, p, p, p, p, p, None,
                                                     None) == -2
+
+
+def test_workspace_for_any_operands_is_enough_for_aligned_ones():
+    import ctypes
+    import random
+    from sparse_moe_layer_sum_b200 import build
+    from sparse_moe_layer_sum_b200._lib import MoEGroupedShape, fn
+    build.build_all()
+    rng = random.Random(3)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    shapes = [(16, 300, 1024, 16), (1, 816, 168, 1710)]      # parts of a tensor-core product
+    shapes += [(log(1, 300), log(1, 8192), log(1, 8192), log(1, 70000)) for _ in range(3000)]
+    more = 0
+    for shape in shapes:
+        s = ctypes.byref(MoEGroupedShape(*shape))
+        for dt in (0, 1):
+            for name, flags in (("grouped_linear", ()), ("grouped_linear_dx", (0,)), ("grouped_linear_dx", (1,)),
+                                ("grouped_linear_dw", ()), ("swiglu_checkpoint", ()), ("swiglu_backward", ())):
+                size = fn("moe_train", f"moe_{name}_workspace_size")
+                one, any_ = size(s, dt, *flags, 1), size(s, dt, *flags, 0)
+                assert any_ >= one, (name, shape, dt)
+                more += any_ > one
+    assert more > 0
