@@ -258,9 +258,12 @@ struct RowParams {
 // Depth after which a partial sum leaves tensor memory and is added to the
 // others in fp32 registers.  The tensor cores cut a sum off at 2^-24 of its
 // size with every 16-deep MMA, always towards zero: 8e-6 of the result after
-// 7168 values, 5e-7 after 512.  Results that are rounded to bf16 do not show
-// it; fp32 ones, and 8-bit codes next to a rounding border, do.
+// 7168 values, 5e-7 after 512.  fp32 results, and 8-bit codes next to a rounding
+// border, show it; results that are rounded to bf16 do not until the sum is
+// long: LONG_SUM values of one sign lose some 2^-12, a sixteenth of bf16's own
+// half step, and longer sums leave tensor memory too.
 constexpr int SEG = 512 / BK;
+constexpr int LONG_SUM = 1 << 16;
 
 // k-blocks of the i-th segment of a tile of nkb.  BWD ends a tile with
 // arithmetic that takes the MMAs of several segments, and the MMAs may run two
@@ -886,16 +889,17 @@ struct DwParams {
   int accumulate;
   int passes;     // 1, or SPLIT_PASSES for split operands
   int splits;     // parts of each group's rows, each with its own dw
+  int above, upto;  // the groups of more than `above` rows and at most `upto`
   int tma_store;  // rows of dw are multiples of 16 bytes, dw is 16-byte aligned
   int32_t *status;
 };
 
 // A tile of AT * 256 features of dy (AT blocks of 128 per SM of the pair) by
 // 256 columns of x.
-template <typename TO, int AT>
+// SEGS: sums in segments.
+template <typename TO, int AT, bool SEGS>
 struct DwCfg {
   static constexpr int EPI = 8, NT = 32 * (4 + EPI);
-  static constexpr bool SEGS = sizeof(TO) == 4;  // sums in segments (see SEG)
   static constexpr int FEAT = AT * 256;
   static constexpr int STAGE = AT * TILE + 128 * BK * 2;  // per SM: AT * 128 + 128 columns
   static constexpr int STAGES = AT == 2 ? 4 : 6;          // 192 KB in flight
@@ -910,12 +914,21 @@ struct DwCfg {
   static_assert(BYTES <= 232448, "shared memory");
 };
 
-template <typename TO, int AT>
-__global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
+template <typename TO, int AT, bool SEGS>
+__global__ void __launch_bounds__(DwCfg<TO, AT, SEGS>::NT, 1)
     dw_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmC, const DwParams p) {
-  using C = DwCfg<TO, AT>;
+  using C = DwCfg<TO, AT, SEGS>;
   constexpr int STAGES = C::STAGES;
+  if (p.above >= 0) {  // nothing to do where no group is so long
+    bool any = false;
+    for (int g = threadIdx.x; g < p.G; g += C::NT) {
+      int lo, n;
+      group_bounds(p.offsets, g, p.rows, lo, n, nullptr);
+      any |= n > p.above;
+    }
+    if (!__syncthreads_or(any)) return;
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = align_smem(smem_raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::BAR), *empty = full + STAGES;
@@ -964,6 +977,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     int g, n0, k0, lo, kc;  // g: plane of dw, of split s and group g' s * G + g'
     int kb0, kb, tail;  // k-blocks of one pass and of all; rows of a pass's last one
     int nmma;           // columns of the MMA
+    bool other;         // not a group of this launch (kb 0)
     // rows of k-block b of a pass, and whether it ends inside a 16-row step
     __device__ __forceinline__ int depth(int b) const { return b == kb0 - 1 ? tail : BK; }
     __device__ __forceinline__ bool fix(int b) const { return depth(b) % 16 != 0; }
@@ -976,6 +990,8 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     j.k0 = local % ktiles * 256;
     const int split = p.splits == 1 ? 0 : j.g / p.G;
     group_bounds(p.offsets, j.g - split * p.G, p.rows, j.lo, j.kc, threadIdx.x == 0 ? p.status : nullptr);
+    j.other = j.kc <= p.above || j.kc > p.upto;
+    if (j.other) j.kc = 0;
     if (p.splits > 1) {  // whole k-blocks of the group's rows
       const int part = ((j.kc + p.splits - 1) / p.splits + BK - 1) / BK * BK;
       const int skip = min(j.kc, split * part);
@@ -1051,7 +1067,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
           const uint32_t idesc = idesc_bf16_f32(256, j.nmma) | A_MN | B_MN;
           uint32_t d = 0;
           for (int i = 0, blk = 0; i < j.kb; ++i, blk = blk + 1 == j.kb0 ? 0 : blk + 1) {
-            const bool first = i == 0 || (C::SEGS && i % SEG == 0);
+            const bool first = i == 0 || (SEGS && i % SEG == 0);
             if (first) {
               if (i > 0) {
                 commit<2>(accf + acc.stage);
@@ -1141,7 +1157,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
     };
     for (int64_t tile = unit; tile < total; tile += nunits) {
       const Job j = job(tile);
-      if (j.kb == 0 && p.accumulate) continue;
+      if (j.other || (j.kb == 0 && p.accumulate)) continue;
       // lane l stores columns k0 .. k0 + CH - 1 of feature n0 + l; `word(i)`
       // is the i-th 4-byte word of its row of the staging buffer
       auto store = [&](int n0, int k0, auto word) {
@@ -1253,7 +1269,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT>::NT, 1)
           }
         continue;
       }
-      if (C::SEGS || j.kb == 0) {
+      if (SEGS || j.kb == 0) {
         float sum[NCH][CH];
 #pragma unroll
         for (int c = 0; c < NCH; ++c)

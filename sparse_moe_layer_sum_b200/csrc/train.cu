@@ -355,13 +355,16 @@ bool wide(const RowJob &j, int bn, int feat) {
 
 template <int OP, typename TO>
 moe_status tc_rows(const RowJob &j) {
-  if constexpr (sizeof(TO) == 4) {  // fp32 results: sums in segments
+  // fp32 results, and long sums: in segments
+  if (sizeof(TO) == 4 || (int64_t)j.contract * (j.x1.p ? 2 : 1) > tcg::LONG_SUM) {
     if (wide(j, 256, 256)) return launch_rows<OP, 2, 1, 256, 6, true, TO>(j);
     return launch_rows<OP, 1, 1, 64, 8, true, TO>(j);
-  } else {
+  }
+  if constexpr (sizeof(TO) == 2) {
     if (wide(j, 256, 512)) return launch_rows<OP, 2, 2, 256, 4, false, TO>(j);
     return launch_rows<OP, 1, 1, 64, 8, false, TO>(j);
   }
+  return MOE_ERR_UNSUPPORTED;  // not reached
 }
 
 // The first matmul with its checkpoint, and the gradients of the hidden rows.
@@ -377,9 +380,10 @@ moe_status tc_bwd(const RowJob &j) {
   return launch_rows<tcg::BWD, 1, 1, 64, 8, true, TO>(j);
 }
 
-template <typename TO, int AT>
-moe_status launch_dw(const Product &p, const Operand *ops, int terms, int splits = 1) {
-  using C = tcg::DwCfg<TO, AT>;
+template <typename TO, int AT, bool SEGS>
+moe_status launch_dw(const Product &p, const Operand *ops, int terms, int splits = 1, int above = -1,
+                     int upto = INT32_MAX) {
+  using C = tcg::DwCfg<TO, AT, SEGS>;
   const auto *s = p.s;
   const uint64_t rows = (uint64_t)terms * s->rows;
   const bool store = aligned(p.out, 16) && (int64_t)s->k * sizeof(TO) % 16 == 0;
@@ -390,17 +394,22 @@ moe_status launch_dw(const Product &p, const Operand *ops, int terms, int splits
   c = a;
   if (store && !tensor_map(&c, p.out, p.out_dt, (uint64_t)splits * s->groups, s->n, s->k, 32)) return MOE_ERR_CUDA;
   const tcg::DwParams d{p.offsets, s->groups, s->n, s->k, s->rows, p.out, p.accumulate,
-                        terms == 1 ? 1 : tcg::SPLIT_PASSES, splits, store, p.status};
+                        terms == 1 ? 1 : tcg::SPLIT_PASSES, splits, above, upto, store, p.status};
   const int64_t tiles = (int64_t)s->groups * splits * ((s->n + C::FEAT - 1) / C::FEAT) * ((s->k + 255) / 256);
-  return launch_persistent<tcg::dw_gemm<TO, AT>>(C::NT, (size_t)C::BYTES, 2, tiles, p.stream, a, b, c, d);
+  return launch_persistent<tcg::dw_gemm<TO, AT, SEGS>>(C::NT, (size_t)C::BYTES, 2, tiles, p.stream, a, b, c, d);
 }
 
 moe_status tc_dw(const Product &p, const Operand *ops, int terms) {
-  if (p.out_dt == MOE_F32) return launch_dw<float, 1>(p, ops, terms);
+  if (p.out_dt == MOE_F32) return launch_dw<float, 1, true>(p, ops, terms);
   // a bf16 sum with what is there already adds in fp32, which the packed
   // results of the wider tile no longer are
-  if (p.accumulate || p.s->n <= 256) return launch_dw<bf16, 1>(p, ops, terms);
-  return launch_dw<bf16, 2>(p, ops, terms);
+  const bool narrow = p.accumulate || p.s->n <= 256;
+  if (p.s->rows <= tcg::LONG_SUM)
+    return narrow ? launch_dw<bf16, 1, false>(p, ops, terms) : launch_dw<bf16, 2, false>(p, ops, terms);
+  // groups that may be long: those that are, by a launch whose sums go in segments
+  const moe_status st = narrow ? launch_dw<bf16, 1, false>(p, ops, terms, 1, -1, tcg::LONG_SUM)
+                               : launch_dw<bf16, 2, false>(p, ops, terms, 1, -1, tcg::LONG_SUM);
+  return st != MOE_OK ? st : launch_dw<bf16, 1, true>(p, ops, terms, 1, tcg::LONG_SUM);
 }
 
 // ---------------------------------------------------- operands of the products
@@ -599,7 +608,7 @@ moe_status run_dw(const Product &p) {
     q.out = static_cast<uint8_t *>(p.ws) + pl.bytes;
     q.out_dt = MOE_F32;
     q.accumulate = 0;
-    const moe_status st = launch_dw<float, 1>(q, o, pl.terms, pl.splits);
+    const moe_status st = launch_dw<float, 1, true>(q, o, pl.terms, pl.splits);
     return st != MOE_OK ? st : join(pl, p, (int64_t)p.s->groups * p.s->n, p.s->k, nullptr);
   }
   return tc_dw(p, o, pl.terms);

@@ -105,3 +105,60 @@ def test_smallest_fp32_operands(sizes, n, k):
     v, e = R.linear(x, w, off)
     lost = R.linear(torch.ones_like(x), w.abs(), off)[0] * 2.0 ** -134
     R.assert_close(y, v, e + 1.01 * lost)
+
+
+def positive(seed, rows, cols, by):
+    """Positive values, each row or column (by: 0, 1) with a magnitude of its
+    own, so that long sums of them lie anywhere between two bf16 values."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    v = torch.rand(rows, cols, generator=g, device="cuda", dtype=F32).add_(0.5)
+    m = torch.rand((rows, 1) if by == 0 else (1, cols), generator=g, device="cuda").add_(1.0)
+    return v.mul_(m).to(BF)
+
+
+def assert_rounded(got, want, cut):
+    """bf16 results of long sums of one sign: roundings to nearest (2^-8)
+    average out, to 2^-8 / sqrt(n) or so; what the sums are cut by does not.
+    cut: how much that may be, on average and at most."""
+    rel = (got.double() - want) / want
+    assert rel.abs().max() <= 2.0 ** -8 * (1 + cut) + cut
+    assert got.numel() > 2 ** 17 and rel.mean().abs() < cut
+
+
+# in segments of 512 values: 32 cuts by at most 2^-23 of the sum each, and 2^9
+# fp32 additions to nearest; in one go up to 2^16 values: 2^12 such cuts
+SEGMENTS, WHOLE = 2.0 ** -14, 2.0 ** -11
+
+
+@pytest.mark.parametrize("rows,F", [(640, 1024), (4096, 2048)])    # narrow and wide tiles
+def test_long_contractions_round_once(rows, F):
+    k = 1 << 17
+    x, w = positive(1, rows, k, 0), positive(2, F, k, 0)[None]
+    want = x.double() @ w[0].double().T
+    assert_rounded(moe.grouped_linear(x, w, offs([0, rows])), want, SEGMENTS)
+    w = w.transpose(1, 2).contiguous()
+    assert_rounded(moe.grouped_linear_dx(x, w, offs([0, rows])), want, SEGMENTS)
+    # of two products, each within the length that one may have
+    h = k // 2
+    a, b = x[:, :h].contiguous(), x[:, h:].contiguous()
+    got = moe.grouped_linear_dx(a, w[:, :h].contiguous(), offs([0, rows]), dy2=b, w2=w[:, h:].contiguous())
+    assert_rounded(got, want, SEGMENTS)
+
+
+@pytest.mark.parametrize("n,accumulate", [(1600, False), (1600, True), (200, False)])
+def test_dw_of_very_long_groups_rounds_once(n, accumulate):
+    """Long groups between short and empty ones; a length at the border."""
+    sizes, k = [300, 0, 200001, 1 << 16, 77], 1536 if n > 256 else 1544
+    off = R.offsets_of(sizes)
+    dy, x = positive(1, off[-1], n, 1), positive(2, off[-1], k, 1)
+    st = status()
+    base = torch.ones(len(sizes), n, k, dtype=BF, device="cuda")
+    got = moe.grouped_linear_dw(dy, x, offs(off), out=base.clone(), accumulate=accumulate, status=st)
+    for g, r in R.groups(off):
+        want = dy[r].double().T @ x[r].double() + float(accumulate)
+        if r.stop - r.start > 300:
+            assert_rounded(got[g], want, SEGMENTS if g == 2 else WHOLE)
+        else:
+            e = (r.stop - r.start + 2) * R.ULP * want
+            R.assert_close(got[g], want.cpu(), e.cpu())
+    assert int(st.item()) == 0
