@@ -2,8 +2,8 @@
 
 Argument marshalling only, as in moe.py.  Row buffers are expert-contiguous:
 group g owns rows offsets[g] .. offsets[g + 1] - 1, the order dispatch_build
-produces.  Every function allocates its outputs (or takes them as `out`),
-enqueues on the current stream of the operands' device and does not
+produces.  Every function allocates its outputs (or takes them as `out`, apart
+from the operands), enqueues on the current stream of the operands' device and does not
 synchronise; rows outside the groups are left as they were.
 
     y  = grouped_linear(x, w, offsets)                    # y = x w^T, by group
@@ -107,15 +107,29 @@ def _dtype(t: torch.Tensor, *others: torch.Tensor) -> int:
     return dt
 
 
-def _out(out, out_dtype, dtype, dev: int, *shape: int):
+def _apart(out: torch.Tensor, operands) -> None:
+    """Refuse an `out` that shares memory with what the call reads: blocks that
+    finish early would overwrite operands of the others."""
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    for t in operands:
+        if t is None or lo == hi:
+            continue
+        at = t.data_ptr()
+        if at < hi and lo < at + t.numel() * t.element_size():
+            raise ValueError("out must not share memory with an operand")
+
+
+def _out(out, out_dtype, dtype, dev: int, operands, *shape: int):
     """(`out` or a new tensor, its dtype code) for a result of `shape`, in
-    out_dtype or else `dtype`."""
+    out_dtype or else `dtype`, apart from the operands."""
     if out is None:
         dtype = out_dtype or dtype
     elif out.shape != shape or (out_dtype or out.dtype) != out.dtype:
         raise ValueError("out has another shape or dtype")
     else:
         dtype = out.dtype
+        _apart(out, operands)
     dt = _DT.get(dtype)
     if dt is None:
         raise ValueError("outputs must be bf16 or fp32")
@@ -165,7 +179,7 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
         raise ValueError("x must be [rows, k] and w [groups, n, k]")
     dt = _dtype(x, w)
     (rows, k), n = xs, wsh[1]
-    out, odt = _out(out, out_dtype, x.dtype, dev, rows, n)
+    out, odt = _out(out, out_dtype, x.dtype, dev, (x, w, offsets), rows, n)
     shape, ws, at, nws = _plan("moe_grouped_linear_workspace_size", dev, G, n, k, rows, dt, (x, w))
     _call(dev, "moe_grouped_linear", shape, x.data_ptr(), dt, w.data_ptr(), offsets.data_ptr(),
           out.data_ptr(), odt, at, nws, _status(status))
@@ -190,7 +204,7 @@ def grouped_linear_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, 
     operands = (dy, w, dy2, w2) if two else (dy, w)
     dt = _dtype(*operands)
     (rows, n), k = ys, wsh[2]
-    out, odt = _out(out, out_dtype, dy.dtype, dev, rows, k)
+    out, odt = _out(out, out_dtype, dy.dtype, dev, (*operands, offsets), rows, k)
     shape, ws, at, nws = _plan("moe_grouped_linear_dx_workspace_size", dev, G, n, k, rows, dt, operands,
                                int(two))
     _call(dev, "moe_grouped_linear_dx", shape, dy.data_ptr(), dt, w.data_ptr(), _ptr(dy2), _ptr(w2),
@@ -213,7 +227,7 @@ def grouped_linear_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, 
     _need(out is not None or not accumulate, "accumulate needs out")
     dt = _dtype(dy, x)
     (rows, n), k = ys, xs[1]
-    out, odt = _out(out, out_dtype, dy.dtype, dev, G, n, k)
+    out, odt = _out(out, out_dtype, dy.dtype, dev, (dy, x, offsets), G, n, k)
     shape, ws, at, nws = _plan("moe_grouped_linear_dw_workspace_size", dev, G, n, k, rows, dt, (dy, x))
     _call(dev, "moe_grouped_linear_dw", shape, dy.data_ptr(), dt, x.data_ptr(), offsets.data_ptr(),
           out.data_ptr(), odt, int(accumulate), at, nws, _status(status))
@@ -261,7 +275,7 @@ def restore_rows(ckpt: Checkpoint, index: Optional[torch.Tensor] = None, *,
     if index is not None:
         _need(index.dtype == torch.int32 and index.dim() == 1, "index must be int32 [n]")
     n = rows if index is None else index.numel()
-    out, odt = _out(out, None, dtype, dev, n, k)
+    out, odt = _out(out, None, dtype, dev, (ckpt.codes, ckpt.exps, index), n, k)
     _call(dev, "moe_restore_rows", ckpt.codes.data_ptr(), ckpt.exps.data_ptr(), rows, k,
           _ptr(index), n, out.data_ptr(), odt, _status(status))
     return out
@@ -326,7 +340,7 @@ def gather_rows(src: torch.Tensor, index: torch.Tensor, *, dtype: Optional[torch
           "src must be [rows, k] and index int32 [n]")
     dt = _dtype(src)
     (rows, k), n = src.shape, index.numel()
-    out, odt = _out(None, dtype, src.dtype, dev, n, k)
+    out, odt = _out(None, dtype, src.dtype, dev, (), n, k)
     _call(dev, "moe_gather_rows", src.data_ptr(), dt, rows, k, index.data_ptr(), n, out.data_ptr(),
           odt, _status(status))
     return out

@@ -162,3 +162,22 @@ def test_dw_of_very_long_groups_rounds_once(n, accumulate):
             e = (r.stop - r.start + 2) * R.ULP * want
             R.assert_close(got[g], want.cpu(), e.cpu())
     assert int(st.item()) == 0
+
+
+def test_results_over_their_operands_are_refused():
+    x, w = R.normal(1, 40, 64).cuda(), R.normal(2, 2, 64, 64).cuda()
+    o, dw = offs([0, 20, 40]), torch.zeros(2, 64, 64, dtype=BF, device="cuda")
+    both = torch.zeros(80, 64, dtype=BF, device="cuda")
+    codes = both.view(torch.uint8).view(-1)[:40 * 64].view(40, 64)
+    exps = torch.zeros(40, 2, dtype=torch.uint8, device="cuda")
+    for call in (lambda: moe.grouped_linear(x, w, o, out=x),
+                 lambda: moe.grouped_linear(both[1:41], w, o, out=both[40:]),
+                 lambda: moe.grouped_linear_dx(x, w, o, out=x),
+                 lambda: moe.grouped_linear_dx(x, w, o, dy2=both[:40], w2=w, out=both[39:79]),
+                 lambda: moe.grouped_linear_dw(dw[0], dw[1], offs([0, 30, 64]), out=dw),
+                 lambda: moe.restore_rows(moe.Checkpoint(codes, exps), out=both[:40])):
+        with pytest.raises(ValueError, match="share memory"):
+            call()
+    # side by side is fine
+    assert moe.grouped_linear(both[:40], w, o, out=both[40:]).data_ptr() == both[40:].data_ptr()
+    assert moe.restore_rows(moe.Checkpoint(codes, exps), out=both[40:]).shape == (40, 64)

@@ -117,3 +117,15 @@ def test_workspace_for_any_operands_is_enough_for_aligned_ones():
                 assert any_ >= one, (name, shape, dt)
                 more += any_ > one
     assert more > 0
+
+
+def test_out_apart_from_the_operands():
+    from sparse_moe_layer_sum_b200.training import _apart
+    buf = torch.zeros(256)
+    x = buf[64:128]
+    for lo, hi in ((64, 128), (0, 65), (127, 200), (0, 256), (80, 81)):
+        with pytest.raises(ValueError, match="share memory"):
+            _apart(buf[lo:hi], (None, torch.zeros(3), x))
+    for lo, hi in ((0, 64), (128, 256), (70, 70)):
+        _apart(buf[lo:hi], (None, x))
+    _apart(buf[64:128], (x[:0],))
