@@ -4,6 +4,7 @@ and short groups among the long ones.  Whole results against 64-bit forms."""
 import pytest
 import torch
 
+import test_gpu_experts_training as step
 import train_ref as R
 import sparse_moe_layer_sum_b200 as moe
 
@@ -181,3 +182,144 @@ def test_results_over_their_operands_are_refused():
     # side by side is fine
     assert moe.grouped_linear(both[:40], w, o, out=both[40:]).data_ptr() == both[40:].data_ptr()
     assert moe.restore_rows(moe.Checkpoint(codes, exps), out=both[40:]).shape == (40, 64)
+
+
+# Shapes for which every product takes the tiles of SM pairs (several pairs have
+# more than one of them), partial tiles of rows and of features, groups of none,
+# of a row and of less than a tile, and contractions that wrap the stage rings
+# many times.  The third is past 64 k-blocks, where backward's first segments
+# are twice as long; its fp32 operands have six times as many.
+WIDE = [([700, 0, 900, 33, 65, 130], 1304, 1096),
+        ([257, 513, 1, 700, 0, 300, 255], 2056, 584),
+        ([600, 0, 410, 1, 300], 1544, 4232),
+        ([700, 0, 900, 33, 65, 130], 1301, 1099)]   # off the pitch: through padded copies
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sizes,n,k", WIDE)
+def test_wide_products(sizes, n, k, dtype, out):
+    off = R.offsets_of(sizes, first=2)
+    rows, G = off[-1] + 3, len(sizes)
+    x, dy, dy2 = (R.normal(i, rows, c, dtype=dtype) for i, c in ((1, k), (2, n), (3, n)))
+    w, w2 = (R.normal(i, G, n, k, dtype=dtype, std=k ** -0.5) for i in (4, 5))
+    xd, dyd, dy2d, wd, w2d = (t.cuda() for t in (x, dy, dy2, w, w2))
+    o, st = offs(off), status()
+    live = slice(off[0], off[-1])
+    y = torch.full((rows, n), 7.0, dtype=out, device="cuda")
+    d = torch.full((rows, k), 7.0, dtype=out, device="cuda")
+    for got, (want, e), what in (
+            (moe.grouped_linear(xd, wd, o, out=y, status=st), R.linear(x, w, off), "linear"),
+            (moe.grouped_linear_dx(dyd, wd, o, out=d, status=st), R.dx(dy, w, off), "dx"),
+            (moe.grouped_linear_dx(dyd, wd, o, dy2=dy2d, w2=w2d, out_dtype=out, status=st),
+             R.dx(dy, w, off, dy2, w2), "dx of two")):
+        R.assert_close(got[live], want[live], e[live], what)
+    for t in (y, d):                                     # rows of no group
+        assert (t[:off[0]] == 7.0).all() and (t[off[-1]:] == 7.0).all()
+    R.assert_close(moe.grouped_linear_dw(dyd, xd, o, out_dtype=out, status=st), *R.dw(dy, x, off), "dw")
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sizes,n,k", WIDE)
+def test_wide_swiglu_backward(sizes, n, k, dtype, gated):
+    off = R.offsets_of(sizes)
+    rows, G = off[-1], len(sizes)
+    dy = R.normal(1, rows, k, dtype=dtype)
+    w2 = R.normal(2, G, k, n, dtype=dtype, std=n ** -0.5)
+    a, u = (moe.checkpoint_rows(R.normal(i, rows, n, dtype=F32, std=2.0).cuda()) for i in (3, 4))
+    gate = torch.rand(rows, generator=torch.Generator().manual_seed(5)) + 0.1
+    st = status()
+    got = moe.swiglu_backward(dy.cuda(), w2.cuda(), a, u, offs(off), gate=gate.cuda() if gated else None,
+                              status=st)
+    assert int(st.item()) == 0
+    dh, e = R.dx(dy, w2, off)
+    av, uv = (R.decode(c.codes.cpu(), c.exps.cpu()) for c in (a, u))
+    gate = gate if gated else torch.ones_like(gate)
+    vals, errs = R.swiglu_grads(av, uv, dh, e, gate.to(R.F64), dtype)
+    for g, v, b, name in zip(got, vals, errs, ("da", "du", "hg", "dgate")):
+        R.assert_close(g, v, b, name)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_wide_swiglu_checkpoint(dtype):
+    sizes, n, k = WIDE[2]
+    off = R.offsets_of(sizes)
+    x = R.normal(1, off[-1], k, dtype=dtype)
+    w1, w3 = (R.normal(i, len(sizes), n, k, dtype=dtype, std=2 * k ** -0.5) for i in (2, 3))
+    h, a, u = moe.swiglu_checkpoint(x.cuda(), w1.cuda(), w3.cuda(), offs(off))
+    (av, ae), (uv, ue) = R.linear(x, w1, off), R.linear(x, w3, off)
+    s = R.silu(av).abs()
+    err = 1.1 * ae * (uv.abs() + ue) + s * ue + s * uv.abs() * (R.sigmoid_rel(av, dtype) + 4 * R.ULP)
+    R.assert_close(h, R.silu(av) * uv, err, "h")
+    for c, v, e in ((a, av, ae), (u, uv, ue)):
+        exps = c.exps.cpu()
+        scale = torch.exp2(exps.to(R.F64) - 127).repeat_interleave(32, 1)[:, :n]
+        # half a step of a code: 2^-4 of the value, or 2^-10 of the scale
+        d = (R.decode(c.codes.cpu(), exps) - v).abs()
+        assert (d <= torch.maximum(2.0 ** -4 * (v.abs() + e), scale * 2.0 ** -10) + e).all()
+
+
+def test_wide_shapes_take_the_wide_tiles():
+    """What train.cu's wide() asks, for each product of WIDE and of the step
+    below: rows a group on average, and tiles for half the 74 SM pairs."""
+    for sizes, n, k in WIDE:
+        rows, G = sum(sizes), len(sizes)
+        assert rows / G > 48
+        # (features, rows of a tile, features of one) of linear, dx and backward
+        for F, bn, feat in ((n, 256, 512), (k, 256, 512), (n, 256, 256), (k, 256, 256), (n, 128, 256)):
+            if F == 584 and feat == 512:
+                continue                      # dx to 584: narrow tiles in bf16
+            assert (rows // bn + min(rows, G)) * -(-F // feat) >= 37, (sizes, F, bn, feat)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_wide_step(dtype):
+    """The experts' forward and backward pass with about 360 rows a group."""
+    step.test_forward_and_backward(dict(T=600, dtype=dtype, dim=1032, inter=1304, n_routed=4, n_groups=1,
+                                        topk_groups=1, topk=2))
+
+
+def test_threads_with_inputs_of_their_own():
+    """Calls at once from several threads and streams, each on other inputs and
+    sizes: a workspace or a plan that two of them shared would show."""
+    import threading
+    torch.cuda.synchronize()
+
+    def inputs(i):
+        sizes, n, k = [[70, 0, 131, 5], [300, 41, 0, 9], [64, 64, 1, 700], [5, 3, 0, 90]][i], 264 + 8 * i, 520
+        off = R.offsets_of(sizes)
+        rows, G, dt = off[-1], len(sizes), F32 if i % 2 else BF
+        t = dict(x=R.normal(10 * i, rows, k, dtype=dt), dy=R.normal(10 * i + 1, rows, k, dtype=dt),
+                 w1=R.normal(10 * i + 2, G, n, k, dtype=dt, std=k ** -0.5),
+                 w3=R.normal(10 * i + 3, G, n, k, dtype=dt, std=k ** -0.5),
+                 w2=R.normal(10 * i + 4, G, k, n, dtype=dt, std=n ** -0.5))
+        return {a: b.cuda() for a, b in t.items()} | {"off": offs(off)}
+
+    def work(t):
+        h, a, u = moe.swiglu_checkpoint(t["x"], t["w1"], t["w3"], t["off"])
+        y = moe.grouped_linear(h, t["w2"], t["off"])
+        da, du, hg, dgate = moe.swiglu_backward(t["dy"], t["w2"], a, u, t["off"])
+        dx = moe.grouped_linear_dx(da, t["w1"], t["off"], dy2=du, w2=t["w3"])
+        return [h, a.codes, u.exps, y, da, du, hg, dgate, dx, moe.grouped_linear_dw(da, t["x"], t["off"]),
+                moe.grouped_linear_dw(t["dy"], hg, t["off"])]
+
+    each = [inputs(i) for i in range(4)]
+    want = [work(t) for t in each]
+    torch.cuda.synchronize()
+    same = [None] * 4
+
+    def loop(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = [work(each[i]) for _ in range(10)]
+        s.synchronize()
+        same[i] = all(torch.equal(a, b) for g in got for a, b in zip(g, want[i]))
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [True] * 4
