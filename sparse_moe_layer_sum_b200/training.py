@@ -446,6 +446,11 @@ def experts_training_backward(shape: BlockShape, params: BlockParams, saved: Sav
           and saved.row_token.numel() == saved.row_gate.numel() == T * (k + shape.n_shared)
           and saved.group_offsets.numel() == shape.n_routed + shape.n_shared + 1,
           "saved is not of a batch of this shape")
+    if accumulate is not None:  # all of them before any is added to
+        for name in ("w1", "w3", "w2"):
+            t, w = getattr(accumulate, "d" + name), getattr(params, name)
+            _need(t.shape == w.shape and t.dtype in _DT and t.device == w.device and t.is_contiguous(),
+                  "accumulate must hold gradients of the weights' shapes")
     st = dict(status=status)
     off = saved.group_offsets
     dyr = gather_rows(dy, saved.row_token, dtype=saved.dtype, **st)

@@ -58,6 +58,20 @@ def test_backward_takes_lists_of_the_saved_batch(shape):
             moe.experts_training_backward(shape, p, s, dy)
 
 
+@pytest.mark.parametrize("name", ["dw1", "dw3", "dw2"])
+def test_no_gradient_is_added_to_when_one_does_not_fit(name):
+    p = params(SHAPE)
+    good = dict(dx=None, dgates=None, dw1=torch.zeros_like(p.w1), dw3=torch.zeros_like(p.w3),
+                dw2=torch.zeros_like(p.w2))
+    with pytest.raises(ValueError, match="CUDA"):         # fits
+        moe.experts_training_backward(SHAPE, p, saved(SHAPE, 16), torch.zeros(16, SHAPE.dim),
+                                      accumulate=moe.ExpertGrads(**good))
+    for bad in (good[name][:-1], good[name].double(), good[name].transpose(1, 2)):
+        with pytest.raises(ValueError, match="accumulate"):
+            moe.experts_training_backward(SHAPE, p, saved(SHAPE, 16), torch.zeros(16, SHAPE.dim),
+                                          accumulate=moe.ExpertGrads(**{**good, name: bad}))
+
+
 @pytest.mark.parametrize("shape", [SHAPE, SHARED], ids=["routed", "shared"])
 def test_combine_reads_within_its_operands(shape):
     T, n = 8, 8 * shape.topk
