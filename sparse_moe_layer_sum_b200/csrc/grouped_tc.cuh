@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256) stage_rows(const TI *__restrict__ src, in
       float q[8];  // what is rounded
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        q[j] = TERMS > 1 && isfinite(v[j]) ? fminf(fmaxf(v[j], -BF16_MAX), BF16_MAX) : v[j];
+        q[j] = TERMS > 1 && t == 0 && isfinite(v[j]) ? fminf(fmaxf(v[j], -BF16_MAX), BF16_MAX) : v[j];
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(q[j], q[j + 1]);
