@@ -920,6 +920,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT, SEGS>::NT, 1)
             const __grid_constant__ CUtensorMap tmC, const DwParams p) {
   using C = DwCfg<TO, AT, SEGS>;
   constexpr int STAGES = C::STAGES;
+  bool idle = false;
   if (p.above >= 0) {  // nothing to do where no group is so long
     bool any = false;
     for (int g = threadIdx.x; g < p.G; g += C::NT) {
@@ -927,7 +928,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT, SEGS>::NT, 1)
       group_bounds(p.offsets, g, p.rows, lo, n, nullptr);
       any |= n > p.above;
     }
-    if (!__syncthreads_or(any)) return;
+    idle = !__syncthreads_or(any);
   }
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = align_smem(smem_raw);
@@ -971,7 +972,7 @@ __global__ void __launch_bounds__(DwCfg<TO, AT, SEGS>::NT, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int ntiles = (p.n + C::FEAT - 1) / C::FEAT, ktiles = (p.k + 255) / 256;
-  const int64_t total = (int64_t)p.G * p.splits * ntiles * ktiles;
+  const int64_t total = idle ? 0 : (int64_t)p.G * p.splits * ntiles * ktiles;
 
   struct Job {
     int g, n0, k0, lo, kc;  // g: plane of dw, of split s and group g' s * G + g'

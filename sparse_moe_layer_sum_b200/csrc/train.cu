@@ -355,7 +355,8 @@ bool wide(const RowJob &j, int bn, int feat) {
 
 template <int OP, typename TO>
 moe_status tc_rows(const RowJob &j) {
-  // fp32 results, and long sums: in segments
+  // fp32 results, and long sums: in segments (65600 values, 640 rows to 1024
+  // 431 -> 438 us, 4096 rows to 2048 774 -> 1029 us)
   if (sizeof(TO) == 4 || (int64_t)j.contract * (j.x1.p ? 2 : 1) > tcg::LONG_SUM) {
     if (wide(j, 256, 256)) return launch_rows<OP, 2, 1, 256, 6, true, TO>(j);
     return launch_rows<OP, 1, 1, 64, 8, true, TO>(j);
@@ -406,7 +407,10 @@ moe_status tc_dw(const Product &p, const Operand *ops, int terms) {
   const bool narrow = p.accumulate || p.s->n <= 256;
   if (p.s->rows <= tcg::LONG_SUM)
     return narrow ? launch_dw<bf16, 1, false>(p, ops, terms) : launch_dw<bf16, 2, false>(p, ops, terms);
-  // groups that may be long: those that are, by a launch whose sums go in segments
+  // Groups that may be long: those that are, by a launch whose sums go in
+  // segments.  2048 x 4096: 32 groups of 2200 rows, none of them long, 831 ->
+  // 836 us; with one of 73728 rows among them 1630 -> 1900 us; one of 200000
+  // rows 2.27 -> 3.11 ms, its results off by at most 2^-19 instead of 7e-4.
   const moe_status st = narrow ? launch_dw<bf16, 1, false>(p, ops, terms, 1, -1, tcg::LONG_SUM)
                                : launch_dw<bf16, 2, false>(p, ops, terms, 1, -1, tcg::LONG_SUM);
   return st != MOE_OK ? st : launch_dw<bf16, 1, true>(p, ops, terms, 1, tcg::LONG_SUM);
