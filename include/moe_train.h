@@ -28,10 +28,14 @@
  *    padded, fp32 operands split into three bf16 terms (results as exact as
  *    fp32 sums of operands that are multiples of 2^-133, as all above 2^-110
  *    are; a result that depends on an infinite fp32 operand may be NaN).
- *    Small ones, and any without a workspace, run on the CUDA cores with fp32
- *    multiply-adds.
+ *    The copies are of whole operands, the weights of groups without rows
+ *    included: as many bytes again for bf16, one and a half times as many for
+ *    fp32.  Small products, and any without a workspace, run on the CUDA cores
+ *    with fp32 multiply-adds.
  *  - Each *_workspace_size takes `aligned`: 1 when every operand of the call
- *    is 16-byte aligned, as fresh allocations are; 0 asks for enough for any.
+ *    is 16-byte aligned, as fresh allocations are; 0 asks for enough for any,
+ *    aligned ones too.
+ *  - Outputs share no memory with operands.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H

@@ -12,8 +12,9 @@
 // while the current one is multiplied.  Products are added in pairs
 // (fma.rn.f32x2, two IEEE fp32 multiply-adds per instruction).
 //
-// Bound by the multiply-add rate where there are enough tiles (T 128 and 64),
-// by the latency of a slice where there are few: T 32 takes slices four times
+// Bound by the multiply-add rate where there are enough tiles (T 128 and 64) of
+// rows that fill them (with a row or two a group most multiply-adds are for rows
+// that do not exist), by the latency of a slice where there are few: T 32 takes slices four times
 // as deep, which four groups of 64 threads multiply at the same time, and adds
 // the four partial tiles in a fixed order at the end.
 #pragma once

@@ -69,7 +69,9 @@ moe_status simt_tiles(const simt::Args &a, cudaStream_t s) {
   };
   if (a.splits > 1) return launch_simt<TI, TO, DIR, 32>(a, tiles(32) * a.splits, nsm, s);
   // the larger tile reuses each operand value more often; the smaller ones
-  // where the larger would leave SMs without work
+  // where the larger would leave SMs without work.  (Empty groups count here:
+  // with many groups of a row or two the larger tiles mostly multiply rows that
+  // do not exist.)
   if (tiles(128) >= 4 * nsm) return launch_simt<TI, TO, DIR, 128>(a, tiles(128), nsm, s);
   if (tiles(64) >= nsm) return launch_simt<TI, TO, DIR, 64>(a, tiles(64), nsm, s);
   return launch_simt<TI, TO, DIR, 32>(a, tiles(32), nsm, s);
@@ -238,7 +240,8 @@ struct Plan {
 // The kinds of product, and the number of operations from which staging beats
 // the CUDA cores, by operand type.  Below, the copies and their launches cost
 // more than they save; dw crosses late because its results off the pitch are
-// stored without TMA.  Measured on 28 random shapes either side, for example
+// stored without TMA.  Measured on 28 random shapes either side, none of them
+// with many groups of few rows, whose weights are all copied; for example
 // linear, bf16: 1.2e7 12.3 (CUDA cores) / 10.6 us (staged), 2.2e8 30 / 13 us;
 // dw, bf16: 2.2e8 18.4 / 18.2 us, 8.3e8 48 / 29 us; linear, fp32: 2e8 16.6 /
 // 16.7 us, 2.1e9 122 / 61 us; backward, fp32: 9e8 52 / 86 us, 2.1e9 121 / 82 us.
@@ -410,7 +413,7 @@ moe_status tc_dw(const Product &p, const Operand *ops, int terms) {
   // Groups that may be long: those that are, by a launch whose sums go in
   // segments.  2048 x 4096: 32 groups of 2200 rows, none of them long, 831 ->
   // 836 us; with one of 73728 rows among them 1630 -> 1900 us; one of 200000
-  // rows 2.27 -> 3.11 ms, its results off by at most 2^-19 instead of 7e-4.
+  // rows 2.27 -> 3.11 ms, where one launch cuts positive sums by 7e-4.
   const moe_status st = narrow ? launch_dw<bf16, 1, false>(p, ops, terms, 1, -1, tcg::LONG_SUM)
                                : launch_dw<bf16, 2, false>(p, ops, terms, 1, -1, tcg::LONG_SUM);
   return st != MOE_OK ? st : launch_dw<bf16, 1, true>(p, ops, terms, 1, tcg::LONG_SUM);

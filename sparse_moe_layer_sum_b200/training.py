@@ -3,8 +3,11 @@
 Argument marshalling only, as in moe.py.  Row buffers are expert-contiguous:
 group g owns rows offsets[g] .. offsets[g + 1] - 1, the order dispatch_build
 produces.  Every function allocates its outputs (or takes them as `out`, apart
-from the operands), enqueues on the current stream of the operands' device and does not
-synchronise; rows outside the groups are left as they were.
+from the operands), enqueues on the current stream of the operands' device and
+does not synchronise; rows outside the groups are left as they were.  Autograd
+does not see these calls, as it does not see the rest of the package: no result
+requires a gradient, whatever the operands do, and the backward pass is called
+by name.
 
     y  = grouped_linear(x, w, offsets)                    # y = x w^T, by group
     dx = grouped_linear_dx(dy, w, offsets)                # dx = dy w
@@ -415,8 +418,10 @@ def experts_training_forward(shape: BlockShape, params: BlockParams, x: torch.Te
                              status: Optional[torch.Tensor] = None):
     """(y [T, dim] fp32, SavedExperts) of the routed experts and the shared one
     for x [T, dim], with the routing of router_forward and dispatch_build.
-    Weights in x's dtype (bf16 or fp32).  y is the ordered sum of moe_combine,
-    bit-reproducible."""
+    Weights in x's dtype (bf16 or fp32), all experts' of the shape: the shards
+    of expert-parallel ranks are refused.  y is the ordered sum of moe_combine,
+    bit-reproducible.  x and the projections are kept in 8 bits, with fp32
+    weights too."""
     _need(x.dim() == 2 and x.shape[1] == shape.dim, "x must be [T, dim]")
     _need(params.w1.dtype == x.dtype and x.dtype in _DT, "training takes weights in x's dtype")
     T, k = x.shape[0], shape.topk
